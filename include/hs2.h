@@ -66,6 +66,7 @@ typedef enum {
 
 typedef uint16_t hs2_bf16;    /* raw bf16 bits */
 typedef uint8_t hs2_fp8e4m3;  /* raw OCP E4M3FN bits */
+typedef uint8_t hs2_q4;       /* bytes of 4-bit cache records (144 each)     */
 
 typedef struct {
   int64_t T;           /* tokens (prefill) or cache capacity (decode)          */
@@ -85,7 +86,9 @@ enum {
   HS2_OP_SPARSE = 3,
   HS2_OP_BLOCK_PREFILL = 4,
   HS2_OP_BLOCK_DECODE = 5,
-  HS2_OP_SPARSE_PLAN = 6  /* bytes of a plan for hs2_sparse_plan (size_t(-1): no plan path) */
+  HS2_OP_SPARSE_PLAN = 6, /* bytes of a plan for hs2_sparse_plan (size_t(-1): no plan path) */
+  HS2_OP_DECODE_ATTN_Q4 = 7,
+  HS2_OP_BLOCK_DECODE_Q4 = 8
 };
 
 /*
@@ -302,6 +305,101 @@ hs2_status hs2_block_decode(int32_t batch, const int64_t* seq_len, const hs2_bf1
                             const hs2_bf16* const* q_sparse, hs2_bf16* const* o_sparse,
                             const hs2_shape* shape, void* workspace, size_t workspace_bytes,
                             void* stream);
+
+/*
+ * New K/V rows written into a decode cache, and cache rows read back as bf16.
+ * No counterpart on the pages, which only name the cache: hs2_bridge_kv_fp8
+ * fills it for a whole prompt, these calls append the rows of a decode step or
+ * of a prompt's chunk, and give hs2_block_prefill_rows the bf16 K/V of a prefix
+ * that is only held quantised.
+ *
+ * Token i (0 <= i < n) has its K row at K + i * ldk and its V row at
+ * V + i * ldv (bf16 [n_kv_heads, 128], heads dense; ldk, ldv in elements,
+ * multiples of 8, at least n_kv_heads * 128, so rows can be cut from those of
+ * a fused projection).  Its place in the cache of `batch` sequences of
+ * shape->T tokens is slot[i], or first + i where slot is NULL; slot s is
+ * position s % T of sequence s / T.  slot: DEVICE int32 [n]; an entry -1 (a
+ * padding row) is skipped, any other outside [0, batch * T) is skipped and
+ * reported as HS2_ERR_BAD_INDEX.  A skipped row writes nothing: the cache
+ * (write) or the row of K and V (read) stays as it was.  The slots of one
+ * write must be distinct (of a slot listed twice the record is unspecified).
+ * n == 0 is valid and launches nothing.  Writing never reads the cache; K and
+ * V may not overlap it.  No workspace.  batch * T <= 2^31 - 1.
+ *
+ * e4m3 cache (that of hs2_block_decode): Kc, Vc [batch, T, n_kv_heads, 128],
+ * scale [batch, T, n_kv_heads] fp32, by the rule of hs2_bridge_kv_fp8; a row
+ * pair that holds an infinity or a NaN gets the scale NaN and zero codes.
+ * Read: bf16(code * scale), with separate scales for K and V (they may alias).
+ *
+ * 4-bit cache: [batch, n_kv_heads, T] records of 144 bytes, 16-byte aligned:
+ *   0..63 K codes, 64..127 V codes, 128..135 four K scales, 136..143 four V
+ *   scales (bf16, one per group of 32 dims, group g = dims 32g .. 32g+31).
+ *   value = (nibble - 8) * scale
+ *   scale = max(bf16(amax / 7), 2^-120), nibble - 8 = x / scale rounded to
+ *   nearest (ties to even), in [-7, 7]; nibble 0 (-8) is never written.
+ *   A group that holds an infinity or a NaN: scale NaN, codes 0.
+ *   Dim 32g + 8t + n of K (n < 8) is nibble 8(4t + g) + n; dim 32g + 4x + j of
+ *   V (j < 4) is nibble 4(4x + g) + j; nibble 2i is the low half of byte i.
+ * Read: bf16((nibble - 8) * scale).
+ */
+hs2_status hs2_cache_write_fp8(const hs2_bf16* K, const hs2_bf16* V, int64_t ldk, int64_t ldv,
+                               const int32_t* slot, int64_t first, int64_t n, hs2_fp8e4m3* Kc,
+                               hs2_fp8e4m3* Vc, float* scale, int32_t batch,
+                               const hs2_shape* shape, void* stream);
+hs2_status hs2_cache_read_fp8(const hs2_fp8e4m3* Kc, const hs2_fp8e4m3* Vc, const float* k_scale,
+                              const float* v_scale, const int32_t* slot, int64_t first, int64_t n,
+                              hs2_bf16* K, hs2_bf16* V, int64_t ldk, int64_t ldv, int32_t batch,
+                              const hs2_shape* shape, void* stream);
+hs2_status hs2_cache_write_q4(const hs2_bf16* K, const hs2_bf16* V, int64_t ldk, int64_t ldv,
+                              const int32_t* slot, int64_t first, int64_t n, hs2_q4* cache,
+                              int32_t batch, const hs2_shape* shape, void* stream);
+hs2_status hs2_cache_read_q4(const hs2_q4* cache, const int32_t* slot, int64_t first, int64_t n,
+                             hs2_bf16* K, hs2_bf16* V, int64_t ldk, int64_t ldv, int32_t batch,
+                             const hs2_shape* shape, void* stream);
+
+/*
+ * Attention of one new token per sequence over the 4-bit cache, with its
+ * log-sum-exp (step S2 at one row per sequence; no counterpart on the pages).
+ * K^, V^ the cache's values as above, for head h of KV head g = h / G:
+ *   s_t = scale * q[b,h] . K^[b,g,t]   (0 <= t < seq_len[b])
+ *   lse[b,h] = ln sum_t exp(s_t),  o[b,h] = sum_t exp(s_t - lse[b,h]) V^[b,g,t]
+ * q, o [batch, n_q_heads, 128] bf16; lse [batch, n_q_heads] fp32.  seq_len:
+ * DEVICE int32 [batch], read when the call runs (a captured step replays with
+ * the lengths of the moment); 0 is a batch row without context (o = 0,
+ * lse = -inf), a length outside [0, shape->T] is taken as the nearest bound and
+ * reported as HS2_ERR_BAD_INDEX.  What the cache holds from seq_len[b] on is
+ * not read.  batch <= 512 (HS2_ERR_UNSUPPORTED otherwise).
+ * Workspace: hs2_workspace_size(HS2_OP_DECODE_ATTN_Q4, shape, batch, 0); it
+ * need not be initialised and serves one call at a time.
+ */
+hs2_status hs2_decode_attn_q4(int32_t batch, const int32_t* seq_len, const hs2_bf16* q,
+                              const hs2_q4* cache, hs2_bf16* o, float* lse,
+                              const hs2_shape* shape, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
+ * Sparse attention of one new token per sequence over lists of positions in
+ * the 4-bit cache (step S4 at decode): as hs2_sparse_attn with K^, V^ of
+ * sequence b for its row.  idx [batch, n_kv_heads, k_global + window] holds
+ * positions in [0, shape->T) of the row's own sequence, -1 skipped, any other
+ * entry skipped and reported as HS2_ERR_BAD_INDEX; a position listed twice
+ * counts twice.  An empty list: o = 0, lse = -inf.  lse nullable.  No
+ * workspace.  batch * n_kv_heads <= 2^28 - 1.
+ */
+hs2_status hs2_sparse_attn_q4(int32_t batch, const hs2_bf16* q, const hs2_q4* cache,
+                              const int32_t* idx, hs2_bf16* o, float* lse, const hs2_shape* shape,
+                              void* stream);
+
+/*
+ * hs2_block_decode over the 4-bit cache: the same step, arguments, limits and
+ * outputs, with `cache` in place of the codes and scales.
+ * Workspace: hs2_workspace_size(HS2_OP_BLOCK_DECODE_Q4, shape, batch, 0).
+ */
+hs2_status hs2_block_decode_q4(int32_t batch, const int64_t* seq_len, const hs2_bf16* q_full,
+                               const hs2_q4* cache, hs2_bf16* o_full, float* lse, int32_t* idx,
+                               int32_t n_sparse, const hs2_bf16* const* q_sparse,
+                               hs2_bf16* const* o_sparse, const hs2_shape* shape, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
 /*
  * One decode step of the block with each sequence's context split over R

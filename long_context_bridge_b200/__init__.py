@@ -17,7 +17,9 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libhs2.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_BAD_INDEX = range(7)
-OP_BRIDGE, OP_FULL_ATTN, OP_SELECT, OP_SPARSE, OP_BLOCK_PREFILL, OP_BLOCK_DECODE, OP_SPARSE_PLAN = range(7)
+(OP_BRIDGE, OP_FULL_ATTN, OP_SELECT, OP_SPARSE, OP_BLOCK_PREFILL, OP_BLOCK_DECODE, OP_SPARSE_PLAN,
+ OP_DECODE_ATTN_Q4, OP_BLOCK_DECODE_Q4) = range(9)
+Q4_RECORD_BYTES = 144   # one token's K and V of one KV head in the 4-bit cache
 
 
 class HS2Error(RuntimeError):
@@ -70,6 +72,14 @@ def _load(path: str = LIB_PATH):
         "hs2_decode_cp_sparse": [I32, C.POINTER(C.c_int64), C.POINTER(C.c_int64),
                                  C.POINTER(C.c_int64), I32, P, P, P, P, P, P, I32, PP, P, SP, P],
         "hs2_decode_cp_finish": [I32, I32, I32, P, PP, SP, P],
+        "hs2_cache_write_fp8": [P, P, I64, I64, P, I64, I64, P, P, P, I32, SP, P],
+        "hs2_cache_read_fp8": [P, P, P, P, P, I64, I64, P, P, I64, I64, I32, SP, P],
+        "hs2_cache_write_q4": [P, P, I64, I64, P, I64, I64, P, I32, SP, P],
+        "hs2_cache_read_q4": [P, P, I64, I64, P, P, I64, I64, I32, SP, P],
+        "hs2_decode_attn_q4": [I32, P, P, P, P, P, SP, P, SZ, P],
+        "hs2_sparse_attn_q4": [I32, P, P, P, P, P, SP, P],
+        "hs2_block_decode_q4": [I32, C.POINTER(C.c_int64), P, P, P, P, P, I32, PP, PP, SP, P, SZ,
+                                P],
     }
     for name, args in sigs.items():
         fn = getattr(L, name)
@@ -97,7 +107,10 @@ EXPORTED = ["hs2_bridge_kv", "hs2_bridge_kv_fp8", "hs2_full_attn_lse", "hs2_sele
             "hs2_debug_set_select_speculation",
             "hs2_decode_cp_attn",
             "hs2_decode_cp_select",
-            "hs2_decode_cp_sparse", "hs2_decode_cp_finish"]
+            "hs2_decode_cp_sparse", "hs2_decode_cp_finish",
+            "hs2_cache_write_fp8", "hs2_cache_read_fp8", "hs2_cache_write_q4",
+            "hs2_cache_read_q4", "hs2_decode_attn_q4", "hs2_sparse_attn_q4",
+            "hs2_block_decode_q4"]
 
 
 def _ptr(t, dtype, what, nullable=False):
@@ -296,6 +309,164 @@ def hs2_decode_cp_finish(n_ranks, sparse_recs, o_sparse, shape: Shape, stream=No
     _check(_lib.hs2_decode_cp_finish(batch, int(n_ranks), len(o_sparse),
                                      _ptr(sparse_recs, F32, "sparse_recs"), os_, C.byref(shape),
                                      _stream(stream)), "hs2_decode_cp_finish")
+
+
+# ---------------------------------------------------------------------------
+# rows into and out of a decode cache; the 4-bit cache
+# ---------------------------------------------------------------------------
+def _rows(t, n_heads, what):
+    """K or V rows [n, n_kv_heads, 128] bf16, dense but for the token stride."""
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dtype != BF16:
+        raise ValueError(f"{what} must be {BF16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != n_heads or t.shape[2] != 128:
+        raise ValueError(f"{what} must be [n, {n_heads}, 128], got {tuple(t.shape)}")
+    st = t.stride()
+    if t.numel() and (st[2] != 1 or (n_heads > 1 and st[1] != 128)):
+        raise ValueError(f"the heads of {what} must be dense (strides [ld, 128, 1])")
+    ld = st[0] if t.shape[0] > 1 else n_heads * 128
+    return C.c_void_p(t.data_ptr()), ld
+
+
+def _shaped(t, shape, what):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what} must be {shape}, got {tuple(t.shape)}")
+
+
+def _one_device(*ts):
+    """The tensors' device; the call runs with it current and, unless a stream
+    is given, on that device's current stream."""
+    dev = ts[0].device
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    return torch.cuda.device(dev)
+
+
+def _row_args(K, V, slot, shape):
+    k, ldk = _rows(K, shape.n_kv_heads, "K")
+    v, ldv = _rows(V, shape.n_kv_heads, "V")
+    n = K.shape[0]
+    if V.shape[0] != n or (slot is not None and tuple(slot.shape) != (n,)):
+        raise ValueError("K, V and slot must hold the same number of tokens")
+    return k, v, ldk, ldv, _ptr(slot, I32T, "slot", True), n
+
+
+def _q4_cache(cache, shape):
+    """Pointer and batch of a 4-bit cache [batch, n_kv_heads, T, 144] uint8."""
+    p = _ptr(cache, U8, "cache")
+    if cache.dim() != 4 or tuple(cache.shape[1:]) != (shape.n_kv_heads, shape.T, Q4_RECORD_BYTES):
+        raise ValueError(f"cache must be [batch, {shape.n_kv_heads}, {shape.T}, {Q4_RECORD_BYTES}],"
+                         f" got {tuple(cache.shape)}")
+    return p, cache.shape[0]
+
+
+def _fp8_cache(Kc, Vc, scales, shape):
+    batch = Kc.shape[0]
+    _shaped(Kc, (batch, shape.T, shape.n_kv_heads, 128), "Kc")
+    _shaped(Vc, (batch, shape.T, shape.n_kv_heads, 128), "Vc")
+    for s in scales:
+        _shaped(s, (batch, shape.T, shape.n_kv_heads), "scale")
+    return batch
+
+
+def hs2_cache_write_q4(K, V, slot, cache, shape: Shape, first=0, stream=None):
+    """Quantises rows K, V [n, n_kv_heads, 128] (any token stride) into the
+    4-bit cache [batch, n_kv_heads, T, 144] at slot [n] int32, or (slot None)
+    at first, first + 1, ...; see include/hs2.h."""
+    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape)
+    c, batch = _q4_cache(cache, shape)
+    with _one_device(cache, K, V, slot):
+        _check(_lib.hs2_cache_write_q4(k, v, ldk, ldv, sl, int(first), n, c, batch, C.byref(shape),
+                                       _stream(stream)), "hs2_cache_write_q4")
+
+
+def hs2_cache_read_q4(cache, slot, K, V, shape: Shape, first=0, stream=None):
+    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape)
+    c, batch = _q4_cache(cache, shape)
+    with _one_device(cache, K, V, slot):
+        _check(_lib.hs2_cache_read_q4(c, sl, int(first), n, k, v, ldk, ldv, batch, C.byref(shape),
+                                      _stream(stream)), "hs2_cache_read_q4")
+
+
+def hs2_cache_write_fp8(K, V, slot, Kc, Vc, scale, shape: Shape, first=0, stream=None):
+    """The e4m3 form of hs2_cache_write_q4: codes Kc, Vc [batch, T, n_kv_heads,
+    128] and one fp32 scale per (token, KV head), the cache of hs2_block_decode."""
+    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape)
+    pk, pv, ps = _ptr(Kc, U8, "Kc"), _ptr(Vc, U8, "Vc"), _ptr(scale, F32, "scale")
+    batch = _fp8_cache(Kc, Vc, (scale,), shape)
+    with _one_device(Kc, Vc, scale, K, V, slot):
+        _check(_lib.hs2_cache_write_fp8(k, v, ldk, ldv, sl, int(first), n, pk, pv, ps, batch,
+                                        C.byref(shape), _stream(stream)), "hs2_cache_write_fp8")
+
+
+def hs2_cache_read_fp8(Kc, Vc, k_scale, v_scale, slot, K, V, shape: Shape, first=0, stream=None):
+    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape)
+    pk, pv = _ptr(Kc, U8, "Kc"), _ptr(Vc, U8, "Vc")
+    pks, pvs = _ptr(k_scale, F32, "k_scale"), _ptr(v_scale, F32, "v_scale")
+    batch = _fp8_cache(Kc, Vc, (k_scale, v_scale), shape)
+    with _one_device(Kc, Vc, k_scale, v_scale, K, V, slot):
+        _check(_lib.hs2_cache_read_fp8(pk, pv, pks, pvs, sl, int(first), n, k, v, ldk, ldv, batch,
+                                       C.byref(shape), _stream(stream)), "hs2_cache_read_fp8")
+
+
+def hs2_decode_attn_q4(seq_len, q, cache, o, lse, shape: Shape, workspace, stream=None):
+    """Attention of one new token per sequence over the 4-bit cache, with its
+    lse; seq_len is a device int32 [batch] tensor read when the call runs."""
+    c, batch = _q4_cache(cache, shape)
+    heads = (batch, shape.n_q_heads, 128)
+    pl, pq, po, ps = (_ptr(seq_len, I32T, "seq_len"), _ptr(q, BF16, "q"), _ptr(o, BF16, "o"),
+                      _ptr(lse, F32, "lse"))
+    _shaped(seq_len, (batch,), "seq_len")
+    _shaped(q, heads, "q")
+    _shaped(o, heads, "o")
+    _shaped(lse, heads[:2], "lse")
+    nbytes = 0 if workspace is None else workspace.numel()
+    with _one_device(cache, seq_len, q, o, lse, workspace):
+        _check(_lib.hs2_decode_attn_q4(batch, pl, pq, c, po, ps, C.byref(shape),
+                                       _ptr(workspace, U8, "workspace", True), nbytes,
+                                       _stream(stream)), "hs2_decode_attn_q4")
+
+
+def hs2_sparse_attn_q4(q, cache, idx, o, lse, shape: Shape, stream=None):
+    """Attention of one new token per sequence over the positions in idx
+    [batch, n_kv_heads, k_global + window] of the 4-bit cache; lse may be None."""
+    c, batch = _q4_cache(cache, shape)
+    heads = (batch, shape.n_q_heads, 128)
+    pq, pi, po, ps = (_ptr(q, BF16, "q"), _ptr(idx, I32T, "idx"), _ptr(o, BF16, "o"),
+                      _ptr(lse, F32, "lse", True))
+    _shaped(q, heads, "q")
+    _shaped(o, heads, "o")
+    _shaped(idx, (batch, shape.n_kv_heads, shape.k_global + shape.window), "idx")
+    if lse is not None:
+        _shaped(lse, heads[:2], "lse")
+    with _one_device(cache, q, idx, o, lse):
+        _check(_lib.hs2_sparse_attn_q4(batch, pq, c, pi, po, ps, C.byref(shape), _stream(stream)),
+               "hs2_sparse_attn_q4")
+
+
+def hs2_block_decode_q4(seq_len, q_full, cache, o_full, lse, idx, q_sparse, o_sparse, shape: Shape,
+                        workspace, stream=None):
+    """hs2_block_decode over the 4-bit cache; seq_len is a host sequence of ints."""
+    c, batch = _q4_cache(cache, shape)
+    if len(seq_len) != batch or len(q_sparse) != len(o_sparse):
+        raise ValueError("seq_len must hold one length per sequence, o_sparse one output per layer")
+    heads = (batch, shape.n_q_heads, 128)
+    pq, po, ps, pi = (_ptr(q_full, BF16, "q_full"), _ptr(o_full, BF16, "o_full"),
+                      _ptr(lse, F32, "lse"), _ptr(idx, I32T, "idx"))
+    for t, what in ((q_full, "q_full"), (o_full, "o_full"), *((t, "q_sparse") for t in q_sparse),
+                    *((t, "o_sparse") for t in o_sparse)):
+        _shaped(t, heads, what)
+    _shaped(lse, heads[:2], "lse")
+    _shaped(idx, (batch, shape.n_kv_heads, shape.k_global + shape.window), "idx")
+    qs, _keep_q = _ptr_array(q_sparse, BF16, "q_sparse")
+    os_, _keep_o = _ptr_array(o_sparse, BF16, "o_sparse")
+    nbytes = 0 if workspace is None else workspace.numel()
+    with _one_device(cache, q_full, o_full, lse, idx, workspace, *q_sparse, *o_sparse):
+        _check(_lib.hs2_block_decode_q4(batch, _i64s(seq_len), pq, c, po, ps, pi, len(q_sparse), qs,
+                                        os_, C.byref(shape), _ptr(workspace, U8, "workspace", True),
+                                        nbytes, _stream(stream)), "hs2_block_decode_q4")
 
 
 def hs2_get_device_status(stream=None) -> int:

@@ -11,7 +11,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhs2.so")
 SOURCES = ["hs2_api.cu", "bridge_gemm.cu", "full_attn.cu", "select_topk.cu", "sparse_attn.cu",
-           "sparse_union.cu", "decode.cu", "probe.cu"]
+           "sparse_union.cu", "decode.cu", "cache.cu", "attn_q4.cu", "probe.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
          "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]

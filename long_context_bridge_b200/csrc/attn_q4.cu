@@ -1,0 +1,549 @@
+// attn_q4.cu -- attention of new tokens over the 4-bit KV cache (q4.cuh): over
+// each sequence's whole context (with its log-sum-exp, and for the block's
+// selection its logits), and over index lists (the sparse layers).
+//
+// decode_attn_q4: grid of kAttnCtas CTAs of four warps.  The contexts' tiles
+// of 128 tokens, in the order (sequence, KV head, tile), are cut into equal
+// contiguous ranges, one per CTA, so ragged lengths leave no SM idle; every
+// CTA works out its range from the lengths.  Each warp owns 32 tokens of a
+// tile and a ring of stages of its own, filled by untiled bulk copies of its
+// records (never past the sequence's length): no warp waits for another until
+// a (sequence, KV head) ends.  There the warps' states are joined and one
+// partial (m, l, o) is written; decode_attn_q4_merge joins the partials.
+//
+// sparse_q4: a cluster of CTAs per (sequence, KV head) splits the list; lanes
+// copy the listed records into shared memory one by one (holes and entries out
+// of range closed up first), and the cluster joins through distributed shared
+// memory.
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "q4.cuh"
+
+namespace hs2 {
+
+HS2_STATUS_ACCESSOR(status_attn_q4)
+HS2_BUDGET_SETTER(budget_attn_q4)
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+constexpr int NW = 4;                       // warps per CTA
+constexpr int WT = 32;                      // tokens per warp and tile
+constexpr int TILE = NW * WT;               // tokens per tile
+constexpr int STAGES = 3;                   // ring depth per warp
+constexpr int STAGE_BYTES = WT * Q4_REC;    // 4608
+
+template <int NT>
+struct JoinBuf {  // the four warps' states of one (sequence, KV head)
+  float m[NW][NT * 8], l[NW][NT * 8];
+  float o[NW][NT * 8][128];
+};
+
+template <int NT>
+constexpr int attn_smem_bytes() {
+  return NW * STAGES * STAGE_BYTES + int(sizeof(JoinBuf<NT>)) + 16;
+}
+
+// length of sequence b, clamped to [0, cap]
+__device__ __forceinline__ int seq_length(const Q4Lens& lens, int b, int64_t cap) {
+  return lens.dev == nullptr ? lens.host[b] : min(max(__ldg(lens.dev + b), 0), int(cap));
+}
+
+// s_pre[b] = tiles of one KV head in sequences before b; s_pre[B] = all
+// (B <= kQ4MaxBatch, 128 threads, a CTA barrier on both sides)
+__device__ void tile_prefix(const Q4Lens& lens, int B, int64_t cap, int* s_pre, int* s_sum) {
+  constexpr int PER = kQ4MaxBatch / (NW * 32);
+  const int tid = threadIdx.x, lane = lane_id();
+  int n[PER], mine = 0;
+  const int per = (B + NW * 32 - 1) / (NW * 32);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int b = tid * per + i;
+    n[i] = i < per && b < B ? (seq_length(lens, b, cap) + TILE - 1) / TILE : 0;
+    // a length outside [0, cap] is reported, and taken as the nearest bound
+    if (i < per && b < B && lens.dev != nullptr && unsigned(__ldg(lens.dev + b)) > unsigned(cap))
+      set_dev_status(DEV_BAD_INDEX);
+    mine += n[i];
+  }
+  int inc = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += v;
+  }
+  if (lane == 31) s_sum[warp_id()] = inc;
+  __syncthreads();
+  int base = inc - mine;
+  for (int w = 0; w < warp_id(); ++w) base += s_sum[w];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int b = tid * per + i;
+    if (i < per && b < B) s_pre[b] = base;
+    base += n[i];
+  }
+  if (tid == 0) {
+    int all = 0;
+    for (int w = 0; w < NW; ++w) all += s_sum[w];
+    s_pre[B] = all;
+  }
+  __syncthreads();
+}
+
+// a position in the flat order (sequence, KV head, tile)
+struct TileAt {
+  int b, g, i, nt, len;  // sequence, KV head, tile; that sequence's tiles and length
+};
+
+__device__ __forceinline__ TileAt tile_at(int64_t flat, const int* s_pre, const Q4Lens& lens,
+                                          int B, int64_t cap, int Hkv) {
+  int lo = 0, hi = B;  // largest b with s_pre[b] * Hkv <= flat (its tiles not empty)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (int64_t(s_pre[mid]) * Hkv <= flat) lo = mid; else hi = mid;
+  }
+  TileAt a;
+  a.b = lo;
+  a.nt = s_pre[lo + 1] - s_pre[lo];
+  a.len = seq_length(lens, lo, cap);
+  const int r = int(flat - int64_t(s_pre[lo]) * Hkv);
+  a.g = r / a.nt;
+  a.i = r - a.g * a.nt;
+  return a;
+}
+
+__device__ __forceinline__ void tile_next(TileAt& a, const int* s_pre, const Q4Lens& lens, int B,
+                                          int64_t cap, int Hkv) {
+  if (++a.i < a.nt) return;
+  a.i = 0;
+  if (++a.g < Hkv) return;
+  a.g = 0;
+  a.nt = 0;
+  while (a.nt == 0 && ++a.b < B) a.nt = s_pre[a.b + 1] - s_pre[a.b];
+  if (a.b < B) a.len = seq_length(lens, a.b, cap);
+}
+
+// Ranges that `total` tiles are cut into: range c is [total c / n, total (c +
+// 1) / n), none of them empty, so that the ranges of one (sequence, KV head)
+// are consecutive and each has written its partial.
+__device__ __forceinline__ int64_t range_count(int64_t total, int ctas) {
+  return total < ctas ? total : ctas;
+}
+
+template <int G, bool LOGITS>
+__global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
+    decode_attn_q4(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict__ cache,
+                   const __grid_constant__ Q4Lens lens, int B, int64_t cap, int Hkv,
+                   float scale_log2, float* __restrict__ logits, float2* __restrict__ part,
+                   float* __restrict__ part_o) {
+  constexpr int NT = G > 8 ? G / 8 : 1;
+  __shared__ int s_pre[kQ4MaxBatch + 1];
+  __shared__ int s_sum[NW];
+  __shared__ uint64_t full[NW][STAGES];
+  extern __shared__ uint8_t dsmem_raw[];
+  uint8_t* dsmem = dsmem_raw + ((16u - (smem_u32(dsmem_raw) & 15u)) & 15u);
+  JoinBuf<NT>& join = *reinterpret_cast<JoinBuf<NT>*>(dsmem + NW * STAGES * STAGE_BYTES);
+
+  const int warp = warp_id(), lane = lane_id(), gid = lane >> 2, t = lane & 3;
+  uint8_t* ring = dsmem + warp * STAGES * STAGE_BYTES;
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (lane == 0) {
+    for (int i = 0; i < STAGES; ++i) mbar_init(&full[warp][i], 1);
+    fence_barrier_init();
+  }
+  tile_prefix(lens, B, cap, s_pre, s_sum);  // its barriers publish the mbarriers too
+  const int64_t total = int64_t(s_pre[B]) * Hkv;
+  const int64_t n_ranges = range_count(total, gridDim.x);
+  if (blockIdx.x >= n_ranges) return;
+  const int64_t t0 = total * blockIdx.x / n_ranges, t1 = total * (blockIdx.x + 1) / n_ranges;
+
+  // tokens of this warp's part of a tile
+  auto count = [&](const TileAt& a) { return min(max(a.len - a.i * TILE - warp * WT, 0), WT); };
+  auto records = [&](const TileAt& a) {
+    return cache + ((int64_t(a.b) * Hkv + a.g) * cap + int64_t(a.i) * TILE + warp * WT) * Q4_REC;
+  };
+  TileAt ahead = tile_at(t0, s_pre, lens, B, cap, Hkv);  // the next tile to copy
+  TileAt at = ahead;
+  int64_t t_ahead = t0;
+  int issued = 0, used = 0;  // stages filled / attended (a tile without tokens takes none)
+  bool ok = true;
+  auto fill = [&]() {  // copies tiles until the ring is full
+    while (ok && t_ahead < t1 && issued - used < STAGES) {
+      const int n = count(ahead);
+      if (n > 0) {
+        if (lane == 0) {
+          const int s = issued % STAGES;
+          mbar_arrive_expect_tx(&full[warp][s], n * Q4_REC);
+          bulk_load(ring + s * STAGE_BYTES, records(ahead), n * Q4_REC, &full[warp][s]);
+        }
+        ++issued;
+      }
+      ++t_ahead;
+      tile_next(ahead, s_pre, lens, B, cap, Hkv);
+    }
+  };
+  fill();
+
+  for (int64_t tt = t0; tt < t1;) {
+    // ---- one (sequence, KV head): tiles at.i .. of it in this CTA's range
+    const int b = at.b, g = at.g;
+    const int64_t seg_end = min(t1, tt + (at.nt - at.i));
+    Q4State<NT> st;
+    q4_init<NT>(st, q + (int64_t(b) * Hkv + g) * G * 128, G, scale_log2);
+    float* lg = LOGITS ? logits + (int64_t(b) * Hkv + g) * cap * G : nullptr;
+    for (; tt < seg_end; ++tt) {
+      const int n = count(at);
+      if (n > 0) {
+        const int s = used % STAGES;
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[warp][s], (used / STAGES) & 1));
+        const int64_t key0 = int64_t(at.i) * TILE + warp * WT;
+#pragma unroll
+        for (int h = 0; h < WT / 16; ++h) {
+          const int nv = n - 16 * h;
+          if (nv <= 0) break;
+          q4_step<NT>(st, ring + s * STAGE_BYTES + h * 16 * Q4_REC, nv, [&](int nt, const float* x) {
+            if constexpr (LOGITS) {
+              const int h0 = nt * 8 + 2 * t;
+              float* r = lg + (key0 + 16 * h + gid) * G + h0;
+              if (h0 + 1 < G) {
+                if (gid < nv) *reinterpret_cast<float2*>(r) = make_float2(x[0], x[1]);
+                if (gid + 8 < nv) *reinterpret_cast<float2*>(r + 8 * G) = make_float2(x[2], x[3]);
+              } else if (h0 < G) {
+                if (gid < nv) r[0] = x[0];
+                if (gid + 8 < nv) r[8 * G] = x[2];
+              }
+            }
+          });
+        }
+        ++used;
+        __syncwarp();  // every lane has read the stage before it is filled again
+        fill();
+      }
+      tile_next(at, s_pre, lens, B, cap, Hkv);
+    }
+    // ---- join the warps and write the partial
+    q4_put<NT>(st, join.m[warp], join.l[warp], join.o[warp]);
+    __syncthreads();
+    const int64_t slot = int64_t(blockIdx.x) + int64_t(b) * Hkv + g;
+    for (int h = warp; h < G; h += NW) {
+      float M = -INFINITY, L = 0.f, w[NW];
+#pragma unroll
+      for (int i = 0; i < NW; ++i) M = fmaxf(M, join.m[i][h]);
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        w[i] = join.m[i][h] == -INFINITY ? 0.f : fast_exp2(join.m[i][h] - M);
+        L += join.l[i][h] * w[i];
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(&join.o[i][h][4 * lane]);
+        acc.x += v.x * w[i];
+        acc.y += v.y * w[i];
+        acc.z += v.z * w[i];
+        acc.w += v.w * w[i];
+      }
+      *reinterpret_cast<float4*>(part_o + (slot * G + h) * 128 + 4 * lane) = acc;
+      if (lane == 0) part[slot * G + h] = make_float2(M, L);
+    }
+    __syncthreads();
+  }
+  // a copy that was issued but never attended (a wait ran out) lands before exit
+  if (lane == 0)
+    for (int s = 0; s < STAGES; ++s)
+      drain_phase(&full[warp][s], issued > s ? (issued - 1 - s) / STAGES + 1 : 0);
+}
+
+// grid (Hkv * G, B), 128 threads: the partials of (b, head) -> o, lse
+__global__ void __launch_bounds__(128)
+    decode_attn_q4_merge(const float2* __restrict__ part, const float* __restrict__ part_o,
+                         const __grid_constant__ Q4Lens lens, int B, int64_t cap, int Hkv, int G,
+                         int n_ctas, __nv_bfloat16* __restrict__ o, float* __restrict__ lse,
+                         float* __restrict__ lse2) {
+  __shared__ int s_pre[kQ4MaxBatch + 1];
+  __shared__ int s_sum[NW];
+  __shared__ float s_red[NW];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int h = blockIdx.x % G, g = blockIdx.x / G, b = blockIdx.y, tid = threadIdx.x;
+  tile_prefix(lens, B, cap, s_pre, s_sum);
+  const int64_t total = int64_t(s_pre[B]) * Hkv;
+  const int nt = s_pre[b + 1] - s_pre[b];
+  const int64_t head = int64_t(b) * Hkv * G + g * G + h;
+  if (nt == 0) {  // an empty context
+    o[head * 128 + tid] = __float2bfloat16_rn(0.f);
+    if (tid == 0) {
+      if (lse != nullptr) lse[head] = -INFINITY;
+      if (lse2 != nullptr) lse2[head] = -INFINITY;
+    }
+    return;
+  }
+  const int64_t S = int64_t(s_pre[b]) * Hkv + int64_t(g) * nt;
+  // the range that holds tile x
+  const int64_t n_ranges = range_count(total, n_ctas);
+  auto cta_of = [&](int64_t x) { return ((x + 1) * n_ranges - 1) / total; };
+  const int64_t c0 = cta_of(S), c1 = cta_of(S + nt - 1);
+  const int64_t base = (c0 + int64_t(b) * Hkv + g) * G + h;
+  const int n = int(c1 - c0 + 1);
+  float M = -INFINITY;
+  for (int i = tid; i < n; i += 128) M = fmaxf(M, part[base + int64_t(i) * G].x);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  if (lane_id() == 0) s_red[warp_id()] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+  float L = 0.f, acc = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) {
+    const float2 p = part[base + int64_t(i) * G];
+    const float w = p.x == -INFINITY ? 0.f : fast_exp2(p.x - M);
+    L += p.y * w;
+    acc += part_o[(base + int64_t(i) * G) * 128 + tid] * w;
+  }
+  o[head * 128 + tid] = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
+  if (tid == 0) {
+    const float l2 = L == 0.f ? -INFINITY : M + __log2f(L);
+    if (lse != nullptr) lse[head] = l2 * kLn2;
+    if (lse2 != nullptr) lse2[head] = l2;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// sparse_q4
+// ---------------------------------------------------------------------------
+constexpr int SST = 4;                       // stages of 16 records per warp
+constexpr int SSTAGE_BYTES = 16 * Q4_REC;    // 2304
+
+template <int NT>
+constexpr int sparse_smem_bytes() {
+  return NW * SST * SSTAGE_BYTES + int(sizeof(JoinBuf<NT>)) + 16;
+}
+
+template <int G, int CS>
+__global__ void __launch_bounds__(NW * 32)
+    sparse_q4(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict__ cache,
+              const int32_t* __restrict__ idx, __nv_bfloat16* __restrict__ O,
+              float* __restrict__ lse, int64_t pairs, int64_t cap, int kw, float scale_log2) {
+  constexpr int NT = G > 8 ? G / 8 : 1;
+  __shared__ uint64_t full[NW][SST];
+  // this CTA's joined state, read by the cluster's first CTA
+  __shared__ float cM[NT * 8], cL[NT * 8];
+  __shared__ float cO[NT * 8][128];
+  extern __shared__ uint8_t dsmem_raw[];
+  uint8_t* dsmem = dsmem_raw + ((16u - (smem_u32(dsmem_raw) & 15u)) & 15u);
+  JoinBuf<NT>& join = *reinterpret_cast<JoinBuf<NT>*>(dsmem + NW * SST * SSTAGE_BYTES);
+  const int warp = warp_id(), lane = lane_id();
+  uint8_t* ring = dsmem + warp * SST * SSTAGE_BYTES;
+  const int64_t pair = blockIdx.x / CS;
+  const int crank = int(blockIdx.x % CS);
+  if (lane == 0) {
+    for (int i = 0; i < SST; ++i) mbar_init(&full[warp][i], 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  // this warp's entries: sixteens part, part + parts, ... of the list
+  const int parts = CS * NW, part = crank * NW + warp;
+  const int32_t* list = idx + pair * kw;
+  const uint8_t* rows = cache + pair * cap * Q4_REC;
+  const int n16 = (kw + 15) / 16;
+  int issued = 0, used = 0;
+  int counts = 0;  // valid records of the stages in flight, 8 bits each
+  bool ok = true;
+  int e16 = part;
+  auto entry = [&](int at16) {
+    const int e = at16 * 16 + lane;
+    return lane < 16 && at16 < n16 && e < kw ? __ldg(list + e) : -1;
+  };
+  int j_next = entry(e16);
+  auto fill = [&]() {
+    while (ok && e16 < n16 && issued - used < SST) {
+      int j = j_next;
+      e16 += parts;
+      j_next = entry(e16);
+      if (j != -1 && unsigned(j) >= unsigned(cap)) {
+        set_dev_status(DEV_BAD_INDEX);
+        j = -1;
+      }
+      const unsigned bal = __ballot_sync(0xffffffffu, j >= 0);
+      const int n = __popc(bal);
+      if (n == 0) continue;
+      const int s = issued % SST;
+      if (lane == 0) mbar_arrive_expect_tx(&full[warp][s], n * Q4_REC);
+      __syncwarp();
+      if (j >= 0)
+        bulk_load(ring + s * SSTAGE_BYTES + __popc(bal & ((1u << lane) - 1u)) * Q4_REC,
+                  rows + int64_t(j) * Q4_REC, Q4_REC, &full[warp][s]);
+      counts = (counts & ~(0xFF << (8 * s))) | (n << (8 * s));
+      ++issued;
+    }
+  };
+  fill();
+  Q4State<NT> st;
+  q4_init<NT>(st, q + pair * G * 128, G, scale_log2);
+  while (used < issued) {
+    const int s = used % SST;
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[warp][s], (used / SST) & 1));
+    q4_step<NT>(st, ring + s * SSTAGE_BYTES, (counts >> (8 * s)) & 0xFF, [](int, const float*) {});
+    ++used;
+    __syncwarp();
+    fill();
+  }
+  q4_put<NT>(st, join.m[warp], join.l[warp], join.o[warp]);
+  __syncthreads();
+  namespace cg = cooperative_groups;
+  for (int h = warp; h < G; h += NW) {
+    float M = -INFINITY, L = 0.f, w[NW];
+#pragma unroll
+    for (int i = 0; i < NW; ++i) M = fmaxf(M, join.m[i][h]);
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      w[i] = join.m[i][h] == -INFINITY ? 0.f : fast_exp2(join.m[i][h] - M);
+      L += join.l[i][h] * w[i];
+    }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(&join.o[i][h][4 * lane]);
+      acc.x += v.x * w[i];
+      acc.y += v.y * w[i];
+      acc.z += v.z * w[i];
+      acc.w += v.w * w[i];
+    }
+    *reinterpret_cast<float4*>(&cO[h][4 * lane]) = acc;
+    if (lane == 0) {
+      cM[h] = M;
+      cL[h] = L;
+    }
+  }
+  cg::cluster_group cluster = cg::this_cluster();
+  if constexpr (CS > 1) cluster.sync(); else __syncwarp();
+  // heads are spread over the cluster's CTAs
+  for (int h = crank + CS * warp; h < G; h += CS * NW) {
+    float m[CS], M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int c = 0; c < CS; ++c) {
+      m[c] = CS > 1 ? *cluster.map_shared_rank(&cM[h], c) : cM[h];
+      M = fmaxf(M, m[c]);
+    }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int c = 0; c < CS; ++c) {
+      const float w = m[c] == -INFINITY ? 0.f : fast_exp2(m[c] - M);
+      L += (CS > 1 ? *cluster.map_shared_rank(&cL[h], c) : cL[h]) * w;
+      const float* src = CS > 1 ? cluster.map_shared_rank(&cO[h][0], c) : &cO[h][0];
+      const float4 v = *reinterpret_cast<const float4*>(src + 4 * lane);
+      acc.x += v.x * w;
+      acc.y += v.y * w;
+      acc.z += v.z * w;
+      acc.w += v.w * w;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;  // an empty list: o = 0, lse = -inf
+    const int64_t head = pair * G + h;
+    *reinterpret_cast<uint2*>(O + head * 128 + 4 * lane) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lse != nullptr && lane == 0) lse[head] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
+  }
+  if constexpr (CS > 1) cluster.sync();  // shared memory stays until it has been read
+  if (lane == 0)
+    for (int s = 0; s < SST; ++s)
+      drain_phase(&full[warp][s], issued > s ? (issued - 1 - s) / SST + 1 : 0);
+}
+
+template <int G, bool LOGITS>
+cudaError_t launch_attn_g(const Q4AttnArgs& a, cudaStream_t st) {
+  constexpr int NT = G > 8 ? G / 8 : 1;
+  const int64_t most = int64_t(a.B) * a.Hkv * ((a.cap + TILE - 1) / TILE);
+  constexpr int kMost = G > 8 ? kQ4AttnCtas * 2 / 3 : kQ4AttnCtas;  // one wave (launch bounds)
+  const int ctas = int(most < kMost ? most : kMost);
+  float2* part = reinterpret_cast<float2*>(a.ws);
+  const int64_t slots = int64_t(kQ4AttnCtas) + int64_t(a.B) * a.Hkv;
+  float* part_o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.ws) +
+                                           (size_t(slots) * G * 8 + 255) / 256 * 256);
+  const auto kernel = decode_attn_q4<G, LOGITS>;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), attn_smem_bytes<NT>());
+  if (e != cudaSuccess) return e;
+  kernel<<<ctas, NW * 32, attn_smem_bytes<NT>(), st>>>(
+      reinterpret_cast<const __nv_bfloat16*>(a.q), a.cache, a.lens, a.B, a.cap, a.Hkv,
+      a.scale * kLog2e, a.logits, part, part_o);
+  // the merge's CTAs may start while the last tiles are attended; they wait
+  // for the whole grid before they read a partial
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(a.Hkv) * G, unsigned(a.B));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, decode_attn_q4_merge, static_cast<const float2*>(part),
+                         static_cast<const float*>(part_o), a.lens, a.B, a.cap, a.Hkv, G, ctas,
+                         reinterpret_cast<__nv_bfloat16*>(a.o), a.lse, a.lse2);
+  if (e != cudaSuccess) return e;
+  count_launch(2);
+  return cudaGetLastError();
+}
+
+template <int G, int CS>
+cudaError_t launch_sparse_cs(const Q4SparseArgs& a, cudaStream_t st) {
+  constexpr int NT = G > 8 ? G / 8 : 1;
+  const auto kernel = sparse_q4<G, CS>;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), sparse_smem_bytes<NT>());
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = int64_t(a.B) * a.Hkv;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(pairs * CS));
+  cfg.blockDim = dim3(NW * 32);
+  cfg.dynamicSmemBytes = sparse_smem_bytes<NT>();
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CS;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, reinterpret_cast<const __nv_bfloat16*>(a.q),
+                         a.cache, a.idx, reinterpret_cast<__nv_bfloat16*>(a.o), a.lse, pairs,
+                         a.cap, a.kw, a.scale * kLog2e);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attn_q4_workspace_bytes(int B, int Hq, int Hkv) {
+  const size_t G = Hq / Hkv, slots = size_t(kQ4AttnCtas) + size_t(B) * Hkv;
+  return (slots * G * 8 + 255) / 256 * 256 + slots * G * 512;
+}
+
+cudaError_t launch_attn_q4(const Q4AttnArgs& a, cudaStream_t st) {
+  switch (a.Hq / a.Hkv) {
+#define HS2_Q4_CASE(G)                                                     \
+  case G:                                                                  \
+    return a.logits != nullptr ? launch_attn_g<G, true>(a, st) : launch_attn_g<G, false>(a, st)
+    HS2_Q4_CASE(1);
+    HS2_Q4_CASE(2);
+    HS2_Q4_CASE(4);
+    HS2_Q4_CASE(8);
+    HS2_Q4_CASE(16);
+#undef HS2_Q4_CASE
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_sparse_q4(const Q4SparseArgs& a, cudaStream_t st) {
+  switch (a.Hq / a.Hkv) {
+    case 1: return launch_sparse_cs<1, 8>(a, st);
+    case 2: return launch_sparse_cs<2, 8>(a, st);
+    case 4: return launch_sparse_cs<4, 8>(a, st);
+    case 8: return launch_sparse_cs<8, 8>(a, st);
+    case 16: return launch_sparse_cs<16, 8>(a, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace hs2

@@ -33,6 +33,10 @@
 //                   the window; an exact radix select over all candidates
 //                   when the list overflows.
 // The sparse layers then gather the FP8 rows at idx (sparse_attn.cu).
+//
+// Over the 4-bit cache (DecodeArgs::cache4) the step is the same with the
+// attention and the sparse layers of attn_q4.cu in place of decode_partial,
+// decode_merge and sparse_attn.cu.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -863,8 +867,15 @@ cudaError_t launch_dec_g(const DecodeArgs& a, const SeqLens& d_seq, int max_len,
   };
   float* logits = reinterpret_cast<float*>(take(size_t(B) * Hkv * a.cap * G * 4));
   float* score = reinterpret_cast<float*>(take(size_t(B) * Hkv * a.cap * 4));
-  Partial* part = reinterpret_cast<Partial*>(take(size_t(B) * Hq * nch * sizeof(Partial)));
-  float* part_o = reinterpret_cast<float*>(take(size_t(B) * Hq * nch * 128 * 4));
+  Partial* part = nullptr;
+  float* part_o = nullptr;
+  uint8_t* ws_q4 = nullptr;
+  if (a.cache4 != nullptr) {
+    ws_q4 = take(attn_q4_workspace_bytes(B, Hq, Hkv));
+  } else {
+    part = reinterpret_cast<Partial*>(take(size_t(B) * Hq * nch * sizeof(Partial)));
+    part_o = reinterpret_cast<float*>(take(size_t(B) * Hq * nch * 128 * 4));
+  }
   float* lse2 = reinterpret_cast<float*>(take(size_t(B) * Hq * 4));
   uint32_t* hist = reinterpret_cast<uint32_t*>(take(size_t(B) * Hkv * NBUCKET * 4));
   // per (b, g): candidate count, finished scoring CTAs, k-th best bucket
@@ -876,7 +887,25 @@ cudaError_t launch_dec_g(const DecodeArgs& a, const SeqLens& d_seq, int max_len,
   cudaError_t e = cudaSuccess;
   unsigned launches = 0;
 
-  if (full || a.step == DEC_CP_ATTN) {
+  if (a.cache4 != nullptr) {
+    // the 4-bit cache: the same step with its own attention (attn_q4.cu)
+    Q4AttnArgs q4{};
+    q4.q = a.q;
+    q4.cache = a.cache4;
+    for (int b = 0; b < B; ++b) q4.lens.host[b] = d_seq.n[b];
+    q4.B = B;
+    q4.cap = a.cap;
+    q4.Hq = Hq;
+    q4.Hkv = Hkv;
+    q4.scale = a.scale;
+    q4.o = a.o;
+    q4.lse = a.lse;
+    q4.lse2 = lse2;
+    q4.logits = logits;
+    q4.ws = ws_q4;
+    e = launch_attn_q4(q4, st);
+    if (e != cudaSuccess) return e;
+  } else if (full || a.step == DEC_CP_ATTN) {
     // K, V codes viewed as [B*cap tokens][Hkv][64 two-byte units]: 64-row boxes
     CUtensorMap tmK, tmV;
     const uint64_t rows = uint64_t(B) * a.cap;
@@ -957,6 +986,15 @@ cudaError_t launch_dec_g(const DecodeArgs& a, const SeqLens& d_seq, int max_len,
   count_launch(launches);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  if (a.cache4 != nullptr) {
+    for (int l = 0; l < a.n_sparse; ++l) {
+      const Q4SparseArgs s{a.qs[l], a.cache4, a.idx,   a.os[l],  nullptr, B,
+                           a.cap,   Hq,       Hkv,     a.scale,  a.k + a.w};
+      e = launch_sparse_q4(s, st);
+      if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+  }
   if (full || a.step == DEC_CP_SPARSE) {
     for (int l = 0; l < a.n_sparse; ++l) {
       SparseArgs s{};
@@ -996,12 +1034,13 @@ cudaError_t launch_dec_g(const DecodeArgs& a, const SeqLens& d_seq, int max_len,
   return cudaSuccess;
 }
 
-size_t dec_ws_bytes(int B, int64_t cap, int Hq, int Hkv) {
+size_t dec_ws_bytes(int B, int64_t cap, int Hq, int Hkv, bool q4) {
   const int G = Hq / Hkv;
   const int nch = int((cap + CH - 1) / CH);
   auto r = [](size_t x) { return (x + 255) / 256 * 256; };
   return r(size_t(B) * Hkv * cap * G * 4) + r(size_t(B) * Hkv * cap * 4) +
-         r(size_t(B) * Hq * nch * sizeof(Partial)) + r(size_t(B) * Hq * nch * 128 * 4) +
+         (q4 ? r(attn_q4_workspace_bytes(B, Hq, Hkv))
+             : r(size_t(B) * Hq * nch * sizeof(Partial)) + r(size_t(B) * Hq * nch * 128 * 4)) +
          r(size_t(B) * Hq * 4) + r(size_t(B) * Hkv * NBUCKET * 4) + r(size_t(B) * Hkv * 12) +
          r(size_t(B) * Hkv * CAPC * 8);
 }
@@ -1011,7 +1050,11 @@ size_t dec_ws_bytes(int B, int64_t cap, int Hq, int Hkv) {
 size_t decode_workspace_bytes(int B, int64_t cap, int Hq, int Hkv, int k, int w) {
   (void)k;
   (void)w;
-  return dec_ws_bytes(B, cap, Hq, Hkv);
+  return dec_ws_bytes(B, cap, Hq, Hkv, false);
+}
+
+size_t decode_q4_workspace_bytes(int B, int64_t cap, int Hq, int Hkv) {
+  return dec_ws_bytes(B, cap, Hq, Hkv, true);
 }
 
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t st) {

@@ -123,6 +123,13 @@ hs2_status cuda_status(cudaError_t e) {
     if (!(cond)) return HS2_ERR_INVALID_ARG;      \
   } while (0)
 
+// a decode cache of `batch` sequences of s->T tokens
+hs2_status check_cache(int32_t batch, const hs2_shape* s) {
+  HS2_NEED(batch > 0);
+  if (int64_t(batch) * s->T > INT32_MAX || s->n_kv_heads > 65535) return HS2_ERR_UNSUPPORTED;
+  return HS2_OK;
+}
+
 // The block calls build and use the union plan slab by slab, so that their
 // workspace does not grow with T beyond the selection's.
 constexpr int64_t kPlanSlabRows = 32768;
@@ -210,6 +217,8 @@ hs2_status hs2_get_device_status(void* stream) {
   v |= status_sparse(true);
   v |= status_sparse_union(true);
   v |= status_decode(true);
+  v |= status_cache(true);
+  v |= status_attn_q4(true);
   if (v == ~0u) return HS2_ERR_CUDA;
   if (v & DEV_TIMEOUT) return HS2_ERR_TIMEOUT;
   if (v & DEV_BAD_INDEX) return HS2_ERR_BAD_INDEX;
@@ -235,13 +244,15 @@ hs2_status hs2_debug_set_wait_budget(int64_t cycles) {
   if (e == cudaSuccess) e = budget_select(c);
   if (e == cudaSuccess) e = budget_sparse_union(c);
   if (e == cudaSuccess) e = budget_decode(c);
+  if (e == cudaSuccess) e = budget_attn_q4(c);
   return cuda_status(e);
 }
 
 size_t hs2_workspace_size(int32_t op, const hs2_shape* s, int32_t batch, int32_t d_model) {
   (void)d_model;
   const bool sel = op == HS2_OP_SELECT || op == HS2_OP_BLOCK_PREFILL ||
-                   op == HS2_OP_BLOCK_DECODE || op == HS2_OP_SPARSE_PLAN;
+                   op == HS2_OP_BLOCK_DECODE || op == HS2_OP_SPARSE_PLAN ||
+                   op == HS2_OP_BLOCK_DECODE_Q4;
   if (check_shape(s, sel) != HS2_OK) return size_t(-1);
   switch (op) {
     case HS2_OP_BRIDGE:
@@ -260,6 +271,12 @@ size_t hs2_workspace_size(int32_t op, const hs2_shape* s, int32_t batch, int32_t
         return size_t(-1);
       return decode_workspace_bytes(batch, s->T, s->n_q_heads, s->n_kv_heads, s->k_global,
                                     s->window);
+    case HS2_OP_DECODE_ATTN_Q4:
+      if (check_cache(batch, s) != HS2_OK || batch > kQ4MaxBatch) return size_t(-1);
+      return attn_q4_workspace_bytes(batch, s->n_q_heads, s->n_kv_heads);
+    case HS2_OP_BLOCK_DECODE_Q4:
+      if (check_cache(batch, s) != HS2_OK || batch > kDecodeMaxBatch) return size_t(-1);
+      return decode_q4_workspace_bytes(batch, s->T, s->n_q_heads, s->n_kv_heads);
   }
   return size_t(-1);
 }
@@ -508,6 +525,179 @@ hs2_status hs2_block_decode(int32_t batch, const int64_t* seq_len, const hs2_bf1
   a.Vc = Vc;
   a.ks = k_scale;
   a.vs = v_scale;
+  a.o = o_full;
+  a.lse = lse;
+  a.idx = idx;
+  a.n_sparse = n_sparse;
+  a.qs = reinterpret_cast<const void* const*>(q_sparse);
+  a.os = reinterpret_cast<void* const*>(o_sparse);
+  a.cap = s->T;
+  a.Hq = s->n_q_heads;
+  a.Hkv = s->n_kv_heads;
+  a.scale = s->scale;
+  a.k = s->k_global;
+  a.w = s->window;
+  a.ws = ws;
+  a.ws_bytes = ws_bytes;
+  return cuda_status(launch_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// rows into and out of a decode cache; the 4-bit cache
+// ---------------------------------------------------------------------------
+}  // extern "C"
+
+namespace {
+
+// checks shared by the four row calls; fills all but the cache's pointers
+hs2_status cache_rows(CacheRowsArgs& a, const void* K, const void* V, int64_t ldk, int64_t ldv,
+                      const int32_t* slot, int64_t first, int64_t n, int32_t batch,
+                      const hs2_shape* s) {
+  HS2_TRY(check_shape(s, false));
+  HS2_TRY(check_cache(batch, s));
+  HS2_NEED(n >= 0 && n <= INT32_MAX);
+  const int64_t row = int64_t(s->n_kv_heads) * 128, slots = int64_t(batch) * s->T;
+  if (slot == nullptr)
+    HS2_NEED(first >= 0 && first <= slots && n <= slots - first);
+  else
+    HS2_NEED((reinterpret_cast<uintptr_t>(slot) & 3) == 0);
+  if (n > 0) {
+    HS2_NEED(K && V && aligned16(K) && aligned16(V));
+    HS2_NEED(ldk >= row && ldv >= row && ldk % 8 == 0 && ldv % 8 == 0);
+  }
+  a.K = K;
+  a.V = V;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.slot = slot;
+  a.first = first;
+  a.n = n;
+  a.cap = s->T;
+  a.n_slots = slots;
+  a.Hkv = s->n_kv_heads;
+  return HS2_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+extern "C" {
+
+hs2_status hs2_cache_write_q4(const hs2_bf16* K, const hs2_bf16* V, int64_t ldk, int64_t ldv,
+                              const int32_t* slot, int64_t first, int64_t n, hs2_q4* cache,
+                              int32_t batch, const hs2_shape* s, void* stream) {
+  CacheRowsArgs a{};
+  HS2_TRY(cache_rows(a, K, V, ldk, ldv, slot, first, n, batch, s));
+  HS2_NEED(cache && aligned16(cache));
+  if (n == 0) return HS2_OK;
+  a.cache = cache;
+  return cuda_status(launch_cache_write(a, static_cast<cudaStream_t>(stream)));
+}
+
+hs2_status hs2_cache_read_q4(const hs2_q4* cache, const int32_t* slot, int64_t first, int64_t n,
+                             hs2_bf16* K, hs2_bf16* V, int64_t ldk, int64_t ldv, int32_t batch,
+                             const hs2_shape* s, void* stream) {
+  CacheRowsArgs a{};
+  HS2_TRY(cache_rows(a, K, V, ldk, ldv, slot, first, n, batch, s));
+  HS2_NEED(cache && aligned16(cache));
+  if (n == 0) return HS2_OK;
+  a.cache = const_cast<hs2_q4*>(cache);
+  return cuda_status(launch_cache_read(a, static_cast<cudaStream_t>(stream)));
+}
+
+hs2_status hs2_cache_write_fp8(const hs2_bf16* K, const hs2_bf16* V, int64_t ldk, int64_t ldv,
+                               const int32_t* slot, int64_t first, int64_t n, hs2_fp8e4m3* Kc,
+                               hs2_fp8e4m3* Vc, float* scale, int32_t batch, const hs2_shape* s,
+                               void* stream) {
+  CacheRowsArgs a{};
+  HS2_TRY(cache_rows(a, K, V, ldk, ldv, slot, first, n, batch, s));
+  HS2_NEED(Kc && Vc && scale && aligned16(Kc) && aligned16(Vc) && aligned4(scale));
+  if (n == 0) return HS2_OK;
+  a.Kc = Kc;
+  a.Vc = Vc;
+  a.ks = scale;
+  return cuda_status(launch_cache_write(a, static_cast<cudaStream_t>(stream)));
+}
+
+hs2_status hs2_cache_read_fp8(const hs2_fp8e4m3* Kc, const hs2_fp8e4m3* Vc, const float* k_scale,
+                              const float* v_scale, const int32_t* slot, int64_t first, int64_t n,
+                              hs2_bf16* K, hs2_bf16* V, int64_t ldk, int64_t ldv, int32_t batch,
+                              const hs2_shape* s, void* stream) {
+  CacheRowsArgs a{};
+  HS2_TRY(cache_rows(a, K, V, ldk, ldv, slot, first, n, batch, s));
+  HS2_NEED(Kc && Vc && k_scale && v_scale && aligned16(Kc) && aligned16(Vc) &&
+           aligned4(k_scale) && aligned4(v_scale));
+  if (n == 0) return HS2_OK;
+  a.Kc = const_cast<hs2_fp8e4m3*>(Kc);
+  a.Vc = const_cast<hs2_fp8e4m3*>(Vc);
+  a.ks = k_scale;
+  a.vs = v_scale;
+  return cuda_status(launch_cache_read(a, static_cast<cudaStream_t>(stream)));
+}
+
+hs2_status hs2_decode_attn_q4(int32_t batch, const int32_t* seq_len, const hs2_bf16* q,
+                              const hs2_q4* cache, hs2_bf16* o, float* lse, const hs2_shape* s,
+                              void* ws, size_t ws_bytes, void* stream) {
+  HS2_TRY(check_shape(s, false));
+  HS2_TRY(check_cache(batch, s));
+  if (batch > kQ4MaxBatch) return HS2_ERR_UNSUPPORTED;
+  HS2_NEED(seq_len && q && cache && o && lse);
+  HS2_NEED(aligned4(seq_len) && aligned16(q) && aligned16(cache) && aligned16(o) && aligned4(lse));
+  if (ws == nullptr || !aligned16(ws) ||
+      ws_bytes < attn_q4_workspace_bytes(batch, s->n_q_heads, s->n_kv_heads))
+    return HS2_ERR_WORKSPACE;
+  Q4AttnArgs a{};
+  a.q = q;
+  a.cache = cache;
+  a.lens.dev = seq_len;
+  a.B = batch;
+  a.cap = s->T;
+  a.Hq = s->n_q_heads;
+  a.Hkv = s->n_kv_heads;
+  a.scale = s->scale;
+  a.o = o;
+  a.lse = lse;
+  a.ws = ws;
+  return cuda_status(launch_attn_q4(a, static_cast<cudaStream_t>(stream)));
+}
+
+hs2_status hs2_sparse_attn_q4(int32_t batch, const hs2_bf16* q, const hs2_q4* cache,
+                              const int32_t* idx, hs2_bf16* o, float* lse, const hs2_shape* s,
+                              void* stream) {
+  HS2_TRY(check_shape(s, true));
+  HS2_TRY(check_cache(batch, s));
+  HS2_NEED(q && cache && idx && o);
+  HS2_NEED(aligned16(q) && aligned16(cache) && aligned4(idx) && aligned16(o) && aligned4(lse));
+  if (int64_t(batch) * s->n_kv_heads > INT32_MAX / 8) return HS2_ERR_UNSUPPORTED;
+  const Q4SparseArgs a{q,    cache,        idx,           o,        lse, batch,
+                       s->T, s->n_q_heads, s->n_kv_heads, s->scale, s->k_global + s->window};
+  return cuda_status(launch_sparse_q4(a, static_cast<cudaStream_t>(stream)));
+}
+
+hs2_status hs2_block_decode_q4(int32_t batch, const int64_t* seq_len, const hs2_bf16* q_full,
+                               const hs2_q4* cache, hs2_bf16* o_full, float* lse, int32_t* idx,
+                               int32_t n_sparse, const hs2_bf16* const* q_sparse,
+                               hs2_bf16* const* o_sparse, const hs2_shape* s, void* ws,
+                               size_t ws_bytes, void* stream) {
+  HS2_TRY(check_shape(s, true));
+  HS2_TRY(check_cache(batch, s));
+  if (batch > kDecodeMaxBatch) return HS2_ERR_UNSUPPORTED;
+  HS2_NEED(seq_len && q_full && cache && o_full && lse && idx);
+  HS2_NEED(aligned16(q_full) && aligned16(cache) && aligned16(o_full) && aligned16(lse) &&
+           aligned16(idx));
+  for (int b = 0; b < batch; ++b) HS2_NEED(seq_len[b] >= 1 && seq_len[b] <= s->T);
+  HS2_NEED(n_sparse >= 0 && (n_sparse == 0 || (q_sparse && o_sparse)));
+  for (int l = 0; l < n_sparse; ++l)
+    HS2_NEED(q_sparse[l] && o_sparse[l] && aligned16(q_sparse[l]) && aligned16(o_sparse[l]));
+  if (ws == nullptr || !aligned16(ws) ||
+      ws_bytes < decode_q4_workspace_bytes(batch, s->T, s->n_q_heads, s->n_kv_heads))
+    return HS2_ERR_WORKSPACE;
+  DecodeArgs a{};
+  a.B = batch;
+  a.seq_len_host = seq_len;
+  a.q = q_full;
+  a.cache4 = cache;
   a.o = o_full;
   a.lse = lse;
   a.idx = idx;

@@ -18,6 +18,8 @@ unsigned status_select(bool clear);
 unsigned status_sparse(bool clear);
 unsigned status_sparse_union(bool clear);
 unsigned status_decode(bool clear);
+unsigned status_cache(bool clear);
+unsigned status_attn_q4(bool clear);
 
 // spin budget (cycles) of the bounded waits in each kernel file (testing)
 cudaError_t budget_bridge(long long cycles);
@@ -25,6 +27,7 @@ cudaError_t budget_full_attn(long long cycles);
 cudaError_t budget_select(long long cycles);
 cudaError_t budget_sparse_union(long long cycles);
 cudaError_t budget_decode(long long cycles);
+cudaError_t budget_attn_q4(long long cycles);
 
 // Tensor maps (bf16, 128-byte swizzle, zero fill out of bounds).
 // dims/strides: x fastest; strides in bytes for dims 1.. .
@@ -193,6 +196,7 @@ struct DecodeArgs {
   int B;
   const int64_t* seq_len_host;
   const void* q;
+  const uint8_t* cache4;  // the 4-bit cache (DEC_FULL only), or null: the e4m3 one
   const uint8_t* Kc;
   const uint8_t* Vc;
   const float* ks;
@@ -213,7 +217,66 @@ struct DecodeArgs {
 // decode limits, checked on the host before any launch
 constexpr int kDecodeMaxBatch = 64;
 size_t decode_workspace_bytes(int B, int64_t cap, int Hq, int Hkv, int k, int w);
+size_t decode_q4_workspace_bytes(int B, int64_t cap, int Hq, int Hkv);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
+
+// New K/V rows written into a cache, and cache rows read back (cache.cu).
+// Token i's slot is slot[i] (-1: none), or first + i where slot is null; slot s
+// is position s % cap of sequence s / cap.
+struct CacheRowsArgs {
+  const void* K;  // bf16 rows [n][Hkv][128], ldk / ldv elements apart (read: outputs)
+  const void* V;
+  int64_t ldk, ldv;
+  const int32_t* slot;
+  int64_t first, n;
+  int64_t cap, n_slots;  // tokens per sequence, batch * cap
+  int Hkv;
+  uint8_t* cache;   // 4-bit records [batch][Hkv][cap][144], or null:
+  uint8_t* Kc;      // e4m3 codes [batch * cap][Hkv][128]
+  uint8_t* Vc;
+  const float* ks;  // [batch * cap][Hkv] (written: ks only)
+  const float* vs;
+};
+cudaError_t launch_cache_write(const CacheRowsArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheRowsArgs& a, cudaStream_t stream);
+
+// Attention over the 4-bit cache (attn_q4.cu).
+constexpr int kQ4MaxBatch = 512;
+constexpr int kQ4AttnCtas = 148 * 3;  // CTAs of a whole wave
+struct Q4Lens {  // lengths on the device, or (dev null) by value for up to 64
+  const int32_t* dev;
+  int host[64];
+};
+struct Q4AttnArgs {
+  const void* q;
+  const uint8_t* cache;
+  Q4Lens lens;
+  int B;
+  int64_t cap;
+  int Hq, Hkv;
+  float scale;
+  void* o;        // bf16 [B][Hq][128]
+  float* lse;     // nullable, natural log
+  float* lse2;    // nullable, base 2
+  float* logits;  // nullable: base-2 logits [B][Hkv][cap][G]
+  void* ws;       // attn_q4_workspace_bytes
+};
+size_t attn_q4_workspace_bytes(int B, int Hq, int Hkv);
+cudaError_t launch_attn_q4(const Q4AttnArgs& a, cudaStream_t stream);
+
+struct Q4SparseArgs {
+  const void* q;  // bf16 [B][Hq][128]
+  const uint8_t* cache;
+  const int32_t* idx;  // [B][Hkv][kw]
+  void* o;
+  float* lse;  // nullable
+  int B;
+  int64_t cap;
+  int Hq, Hkv;
+  float scale;
+  int kw;
+};
+cudaError_t launch_sparse_q4(const Q4SparseArgs& a, cudaStream_t stream);
 
 // read-bandwidth probe (measurement only): `reps` passes of 16-byte loads
 cudaError_t launch_read_probe(const void* buf, size_t bytes, int reps, uint32_t* sink,

@@ -1,0 +1,414 @@
+// q4.cuh -- the 4-bit KV cache: its record, and the warp step that attends a
+// tile of records.
+//
+// The cache is [batch][n_kv_heads][capacity] records of 144 bytes; a record is
+// one token's K and V of one KV head:
+//     0 ..  63   K codes, 4 bits each
+//    64 .. 127   V codes
+//   128 .. 135   K scales, bf16, one per group of 32 dims
+//   136 .. 143   V scales
+//   value = (nibble - 8) * scale;  scale = max(bf16(amax / 7), 2^-120),
+//   nibble - 8 = x / scale rounded to nearest even, within [-7, 7]; a group
+//   that holds an infinity or a NaN gets the scale NaN and the codes 0.
+// A head's tokens are contiguous, so its context is one dense stream (untiled
+// bulk copies, whole DRAM bursts), and 144 bytes = 36 words put consecutive
+// rows four banks apart: the fragment loads below need no swizzle.
+//
+// Dims are interleaved so that every mma.sync fragment word is a mask of a
+// loaded word.  K: dim 32 g + 8 t + n (n < 8) is nibble 8 (4 t + g) + n, so
+// lane t's 16 bytes are its 8 dims of each group g.  V: dim 32 g + 4 x + j
+// (j < 4) is nibble 4 (4 x + g) + j, so the lane of output row x finds its
+// four dims of each group in one half word.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace hs2 {
+
+constexpr int Q4_REC = 144, Q4_K = 0, Q4_V = 64, Q4_KS = 128, Q4_VS = 136;
+
+// ---------------------------------------------------------------------------
+// quantising (cache.cu)
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+  return __ldcs(reinterpret_cast<const uint4*>(p));
+}
+__device__ __forceinline__ void stg_stream(void* p, const uint4& v) {
+  __stcs(reinterpret_cast<uint4*>(p), v);
+}
+
+struct Q4Scale {
+  float inv;      // 1 / scale
+  uint32_t bits;  // the scale's bf16 bits
+  bool finite;
+};
+
+// scale of a group whose largest |x| has the bf16 bits a
+__device__ __forceinline__ Q4Scale q4_scale(uint32_t a) {
+  Q4Scale s;
+  s.finite = a < 0x7F80u;
+  const float q = fmaxf(__uint_as_float(a << 16) / 7.f, __uint_as_float(7u << 23));  // 2^-120
+  const __nv_bfloat16 b = __float2bfloat16_rn(q);
+  s.bits = s.finite ? uint32_t(*reinterpret_cast<const uint16_t*>(&b)) : 0x7FC0u;
+  s.inv = 1.f / __uint_as_float(s.bits << 16);
+  return s;
+}
+
+// Eight codes as one word, element n in nibble n.  x / s is formed as x * (1 /
+// s), within 2^-20 of the quotient (|x / s| < 7.04).  x and s have 8
+// significant bits each, so a quotient is a tie k + 1/2 exactly or at least
+// 1 / 510 away from it: snapping to multiples of 2^-11 puts every tie back on
+// itself and moves no other quotient across one.  Adding 1.5 * 2^23 + 8 then
+// rounds to an integer (ties to even) and leaves code + 8 in the low bits.
+__device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], const Q4Scale& s) {
+  constexpr float kSnap = 6144.f;                // 1.5 * 2^12: ulp 2^-11
+  constexpr float kRound = 12582912.f + 8.f;     // ulp 1
+  constexpr uint32_t kBase = 0x4B400000u;        // bits of 12582912
+  uint32_t w = 0;
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+    const float q = __fadd_rn(__fadd_rn(__fmul_rn(x[n], s.inv), kSnap), -kSnap);
+    w += (__float_as_uint(__fadd_rn(q, kRound)) - kBase) << (4 * n);
+  }
+  return s.finite ? w : 0x88888888u;
+}
+
+// (low nibble - 8) as fp32
+__device__ __forceinline__ float q4_value(uint32_t w) {
+  return __uint_as_float(0x4B000000u | (w & 15u)) - 8388616.f;
+}
+
+// ---------------------------------------------------------------------------
+// attending
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// transpose of an 8 x 8 matrix of 16-bit values held as an mma fragment
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// untiled bulk copy global -> shared (16-byte aligned, a multiple of 16 bytes)
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The state of one warp that attends records with the G query heads of one KV
+// head (NT = ceil(G / 8) tiles of eight).  Lane (gid, t) = (lane / 4, lane %
+// 4) owns heads 8 nt + 2 t and + 1 of the logits (keys gid and gid + 8) and of
+// the output (dims by gid).
+//
+// S^T = K q^T in f16: a code u = nibble is taken as the f16 bits 0x000u (u *
+// 2^-24, a subnormal, exact) or 0x00u0 (u * 2^-20); the query's elements that
+// meet the latter carry 2^-4.  The -8 of the code enters as the accumulator's
+// start, -8 * sum of the group's q.  q is scaled by a power of two per head so
+// that its largest element lies in [2^14, 2^15): bf16's 8 bits then stay exact
+// in f16 down to 2^-28 of it.  A group's sum leaves the MMA in fp32 and meets
+// its K scale there, so the logits see no rounding below fp32.
+//
+// The softmax is base 2 against a reference `ref`: p = 2^(x - ref), with ref =
+// the running maximum - 10 and moved only when some x passes it by 14, so p
+// lies below 2^14 and the accumulators are rarely rescaled.
+//
+// O^T += V^T P^T: P is rounded to f16 (2^-12 relative; below 2^-24 of the
+// running maximum by an absolute 2^-35 of it), transposed by movmatrix,
+// multiplied by each group's V scale relative to `r2` (the power of two at or
+// below the largest V scale met so far) and rounded to f16 once more; V's codes
+// are exact in f16.
+template <int NT>
+struct Q4State {
+  uint32_t qf[NT][4][2][2];  // [group][MMA][register]
+  float q8[NT][4][2];        // -8 * sum of the group's q * 2^-24, heads 2t / 2t+1
+  float f[NT][2];            // logit (base 2) = f * scaled sum
+  float ref[NT][2], l[NT][2];
+  float o[NT][8][4];
+  uint32_t r_bits;           // bf16 bits of r2
+  float r_inv;               // 1 / r2
+};
+
+__device__ __forceinline__ float q4_pow2_bits(uint32_t bits) { return __uint_as_float(bits << 16); }
+// 1 / 2^(e - 127) for a power of two with biased exponent e in [1, 254]
+__device__ __forceinline__ float q4_inv_pow2(uint32_t bits) {
+  const uint32_t e = bits >> 7;
+  return __uint_as_float(e < 254 ? (254 - e) << 23 : 0x00400000u);
+}
+
+// q: the G rows of 128 bf16 of this KV head's query heads
+template <int NT>
+__device__ __forceinline__ void q4_init(Q4State<NT>& st, const __nv_bfloat16* __restrict__ q, int G,
+                                        float scale_log2) {
+  const int lane = lane_id(), gid = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int hh = nt * 8 + gid;
+    uint32_t w[4][4];  // [group][pair] dims 32 g + 8 t + 2 pair, + 1
+    uint32_t a = 0;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const uint4 v = hh < G ? __ldg(reinterpret_cast<const uint4*>(q + hh * 128 + 32 * g + 8 * t))
+                             : make_uint4(0, 0, 0, 0);
+      w[g][0] = v.x;
+      w[g][1] = v.y;
+      w[g][2] = v.z;
+      w[g][3] = v.w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        a = max(a, max(w[g][i] & 0x7FFFu, (w[g][i] >> 16) & 0x7FFFu));
+    }
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+    // biased exponent of the head's largest |q|; 2^up brings it to [2^14, 2^15)
+    const int e = int(a >> 7);
+    const int up = e == 255 || a == 0 ? 0 : min(141 - e, 126);
+    const float mul = __uint_as_float(uint32_t(127 + up) << 23);
+    const float back = __uint_as_float(uint32_t(127 - up) << 23);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      float x[8], s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16lo(w[g][i]) * mul;
+        x[2 * i + 1] = bf16hi(w[g][i]) * mul;
+      }
+#pragma unroll
+      for (int n = 0; n < 8; ++n) s += x[n];
+      // MMA m takes nibbles (2m, 2m + 4) and (2m + 1, 2m + 5)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        st.qf[nt][g][m][0] = pack_h2(x[2 * m], x[2 * m + 4]);
+        st.qf[nt][g][m][1] = pack_h2(x[2 * m + 1] * 0.0625f, x[2 * m + 5] * 0.0625f);
+      }
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      s *= -8.f / 16777216.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        st.q8[nt][g][i] = __shfl_sync(0xffffffffu, s, 4 * (2 * t + i));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      st.f[nt][i] = (scale_log2 * 16777216.f) * __shfl_sync(0xffffffffu, back, 4 * (2 * t + i));
+      st.ref[nt][i] = -INFINITY;
+      st.l[nt][i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) st.o[nt][i][0] = st.o[nt][i][1] = st.o[nt][i][2] = st.o[nt][i][3] = 0.f;
+  }
+  st.r_bits = 0x0080u;
+  st.r_inv = q4_inv_pow2(st.r_bits);
+}
+
+// Moves the softmax references up to (maximum - 10) and r2 up to the largest
+// finite V scale's power of two; rescales what was accumulated.
+template <int NT>
+__device__ __forceinline__ void q4_raise(Q4State<NT>& st, const float (&x)[NT][4],
+                                      const uint2 (&vs)[4]) {
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float mx = fmaxf(x[nt][i], x[nt][i + 2]);
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      const float old = st.ref[nt][i], up = fmaxf(old, mx - 10.f);
+      const float al = old == up ? 1.f : fast_exp2(old - up);
+      st.ref[nt][i] = up;
+      st.l[nt][i] *= al;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        st.o[nt][d][i] *= al;
+        st.o[nt][d][i + 2] *= al;
+      }
+    }
+  uint32_t r = 0;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const uint32_t b[4] = {vs[u].x & 0xFFFFu, vs[u].x >> 16, vs[u].y & 0xFFFFu, vs[u].y >> 16};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r = max(r, b[i] < 0x7F80u ? b[i] : 0u);
+  }
+  r = __reduce_max_sync(0xffffffffu, r) & 0x7F80u;
+  if (r > st.r_bits) {
+    const float al = q4_pow2_bits(st.r_bits) * q4_inv_pow2(r);
+    st.r_bits = r;
+    st.r_inv = q4_inv_pow2(r);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int d = 0; d < 8; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st.o[nt][d][i] *= al;
+  }
+}
+
+// Attends the first nv (1 .. 16) of the 16 records at `rec` (shared memory).
+// on_logits(nt, x): the lane's base-2 logits {key gid: heads 2t, 2t+1; key
+// gid + 8: the same}, -inf from key nv on.
+template <int NT, class F>
+__device__ __forceinline__ void q4_step(Q4State<NT>& st, const uint8_t* rec, int nv, F&& on_logits) {
+  const int lane = lane_id(), gid = lane >> 2, t = lane & 3;
+  // ---- S^T
+  const uint8_t* ra = rec + gid * Q4_REC;
+  const uint8_t* rb = ra + 8 * Q4_REC;
+  const uint4 ka = *reinterpret_cast<const uint4*>(ra + Q4_K + 16 * t);
+  const uint4 kb = *reinterpret_cast<const uint4*>(rb + Q4_K + 16 * t);
+  const uint2 sa = *reinterpret_cast<const uint2*>(ra + Q4_KS);
+  const uint2 sb = *reinterpret_cast<const uint2*>(rb + Q4_KS);
+  // V rows of the lane's four keys (B-fragment order) and their scales
+  uint2 vw[4], vs[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int key = 2 * t + (u & 1) + 8 * (u >> 1);
+    const uint8_t* rv = rec + key * Q4_REC;
+    vw[u] = *reinterpret_cast<const uint2*>(rv + Q4_V + 8 * gid);
+    vs[u] = *reinterpret_cast<const uint2*>(rv + Q4_VS);
+    if (key >= nv) vs[u] = make_uint2(0, 0);
+  }
+  float x[NT][4];
+  const uint32_t kw0[4] = {ka.x, ka.y, ka.z, ka.w}, kw1[4] = {kb.x, kb.y, kb.z, kb.w};
+  const float ks0[4] = {bf16lo(sa.x), bf16hi(sa.x), bf16lo(sa.y), bf16hi(sa.y)};
+  const float ks1[4] = {bf16lo(sb.x), bf16hi(sb.x), bf16lo(sb.y), bf16hi(sb.y)};
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t w0 = kw0[g], w1 = kw1[g], v0 = w0 >> 8, v1 = w1 >> 8;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float c[4] = {st.q8[nt][g][0], st.q8[nt][g][1], st.q8[nt][g][0], st.q8[nt][g][1]};
+      mma_f16_16816(c, w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u,
+                    st.qf[nt][g][0][0], st.qf[nt][g][0][1]);
+      mma_f16_16816(c, v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u,
+                    st.qf[nt][g][1][0], st.qf[nt][g][1][1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float s = i < 2 ? ks0[g] : ks1[g];
+        x[nt][i] = g == 0 ? c[i] * s : fmaf(c[i], s, x[nt][i]);
+      }
+    }
+  }
+  // ---- logits, and whether a reference has to move
+  bool raise = false;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[nt][i] *= st.f[nt][i & 1];
+      if (gid + 8 * (i >> 1) >= nv) x[nt][i] = -INFINITY;
+    }
+    on_logits(nt, x[nt]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) raise |= x[nt][i] > st.ref[nt][i & 1] + 14.f;
+  }
+  uint32_t vmax = 0;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) vmax = __vmaxu2(vmax, __vmaxu2(vs[u].x, vs[u].y));
+  const uint32_t top = (st.r_bits | 0x7Fu) * 0x00010001u;
+  raise |= __vmaxu2(vmax, top) != top;
+  if (__any_sync(0xffffffffu, raise)) q4_raise<NT>(st, x, vs);
+  // ---- P: [key][head] -> [head][keys], then times V's scales per group
+  const float vsc[4][4] = {
+      {bf16lo(vs[0].x), bf16hi(vs[0].x), bf16lo(vs[0].y), bf16hi(vs[0].y)},
+      {bf16lo(vs[1].x), bf16hi(vs[1].x), bf16lo(vs[1].y), bf16hi(vs[1].y)},
+      {bf16lo(vs[2].x), bf16hi(vs[2].x), bf16lo(vs[2].y), bf16hi(vs[2].y)},
+      {bf16lo(vs[3].x), bf16hi(vs[3].x), bf16lo(vs[3].y), bf16hi(vs[3].y)}};
+  uint32_t pb[NT][4][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // no key yet: ref = -inf, every x = -inf, p = 0
+      const float ref = st.ref[nt][i & 1];
+      p[i] = fast_exp2(x[nt][i] - (ref == -INFINITY ? 0.f : ref));
+      st.l[nt][i & 1] += p[i];
+    }
+    const uint32_t t0 = movmatrix_trans(pack_h2(p[0], p[1]));
+    const uint32_t t1 = movmatrix_trans(pack_h2(p[2], p[3]));
+    const float2 p01 = __half22float2(*reinterpret_cast<const __half2*>(&t0));
+    const float2 p89 = __half22float2(*reinterpret_cast<const __half2*>(&t1));
+    const float q0 = p01.x * st.r_inv, q1 = p01.y * st.r_inv;
+    const float q2 = p89.x * st.r_inv, q3 = p89.y * st.r_inv;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      pb[nt][g][0] = pack_h2(q0 * vsc[0][g], q1 * vsc[1][g]);
+      pb[nt][g][1] = pack_h2(q2 * vsc[2][g], q3 * vsc[3][g]);
+    }
+  }
+  // ---- O^T: per group two 16-dim tiles; nibble j of a half word = tile j / 2,
+  // row gid + 8 (j % 2).  f16 bits 0x6400 | u = 1024 + u, 0x6400 | u << 4 =
+  // 1024 + 16 u
+  const __half2 k1032 = __float2half2_rn(-1032.f), k16th = __float2half2_rn(0.0625f),
+                k72 = __float2half2_rn(-72.f);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
+    const uint32_t h01 = g < 2 ? __byte_perm(vw[0].x, vw[1].x, sel) : __byte_perm(vw[0].y, vw[1].y, sel);
+    const uint32_t h89 = g < 2 ? __byte_perm(vw[2].x, vw[3].x, sel) : __byte_perm(vw[2].y, vw[3].y, sel);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const uint32_t y0 = m ? h01 >> 8 : h01, y1 = m ? h89 >> 8 : h89;
+      uint32_t a[4] = {(y0 & 0x000F000Fu) | 0x64006400u, (y0 & 0x00F000F0u) | 0x64006400u,
+                       (y1 & 0x000F000Fu) | 0x64006400u, (y1 & 0x00F000F0u) | 0x64006400u};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        __half2 hv = *reinterpret_cast<const __half2*>(&a[i]);
+        hv = (i & 1) ? __hfma2(hv, k16th, k72) : __hadd2(hv, k1032);
+        a[i] = *reinterpret_cast<const uint32_t*>(&hv);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        mma_f16_16816(st.o[nt][2 * g + m], a[0], a[1], a[2], a[3], pb[nt][g][0], pb[nt][g][1]);
+    }
+  }
+}
+
+// Joins the NW warps' states of a CTA.  Per head h < 8 NT: sM, sL (per warp)
+// and sO (times r2) in shared memory; the caller synchronises between this and
+// q4_joined.
+template <int NT>
+__device__ __forceinline__ void q4_put(const Q4State<NT>& st, float* sM, float* sL,
+                                       float (*sO)[128]) {
+  const int lane = lane_id(), gid = lane >> 2, t = lane & 3;
+  const float r2 = q4_pow2_bits(st.r_bits);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float l = st.l[nt][i];
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+      const int h = nt * 8 + 2 * t + i;
+      if (gid == 0) {
+        sM[h] = st.ref[nt][i];
+        sL[h] = l;
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        // dims 32 g + 4 gid + {0, 1, 2, 3} = tiles 2g, 2g + 1, rows gid, gid + 8
+        *reinterpret_cast<float4*>(&sO[h][32 * g + 4 * gid]) =
+            make_float4(st.o[nt][2 * g][i] * r2, st.o[nt][2 * g][i + 2] * r2,
+                        st.o[nt][2 * g + 1][i] * r2, st.o[nt][2 * g + 1][i + 2] * r2);
+      }
+    }
+}
+
+}  // namespace hs2
