@@ -160,70 +160,83 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
   if (blockIdx.x >= n_ranges) return;
   const int64_t t0 = total * blockIdx.x / n_ranges, t1 = total * (blockIdx.x + 1) / n_ranges;
 
-  // tokens of this warp's part of a tile
-  auto count = [&](const TileAt& a) { return min(max(a.len - a.i * TILE - warp * WT, 0), WT); };
-  auto records = [&](const TileAt& a) {
-    return cache + ((int64_t(a.b) * Hkv + a.g) * cap + int64_t(a.i) * TILE + warp * WT) * Q4_REC;
-  };
-  TileAt ahead = tile_at(t0, s_pre, lens, B, cap, Hkv);  // the next tile to copy
+  // ---- this warp's copies: its part of each tile of the range, in order
+  TileAt ahead = tile_at(t0, s_pre, lens, B, cap, Hkv);
   TileAt at = ahead;
-  int64_t t_ahead = t0;
-  int issued = 0, used = 0;  // stages filled / attended (a tile without tokens takes none)
+  int64_t left = t1 - t0;   // tiles still to copy
+  int run = 0;              // of them, tiles of the (sequence, KV head) being copied
+  int rest = 0;             // its tokens from this warp's part of the next tile on
+  const uint8_t* src = nullptr;
+  int s_in = 0, s_out = 0;  // stage filled next / attended next
+  int in_flight = 0;
+  unsigned ph = 0, odd = 0, filled = 0;  // per stage: phase to wait for; fills odd; any
   bool ok = true;
   auto fill = [&]() {  // copies tiles until the ring is full
-    while (ok && t_ahead < t1 && issued - used < STAGES) {
-      const int n = count(ahead);
-      if (n > 0) {
-        if (lane == 0) {
-          const int s = issued % STAGES;
-          mbar_arrive_expect_tx(&full[warp][s], n * Q4_REC);
-          bulk_load(ring + s * STAGE_BYTES, records(ahead), n * Q4_REC, &full[warp][s]);
-        }
-        ++issued;
+    while (left > 0 && in_flight < STAGES) {
+      if (run == 0) {
+        run = int(min(left, int64_t(ahead.nt - ahead.i)));
+        rest = ahead.len - ahead.i * TILE - warp * WT;
+        src = cache + ((int64_t(ahead.b) * Hkv + ahead.g) * cap + int64_t(ahead.i) * TILE + warp * WT) * Q4_REC;
       }
-      ++t_ahead;
-      tile_next(ahead, s_pre, lens, B, cap, Hkv);
+      if (rest > 0) {
+        if (lane == 0) {
+          const uint32_t bytes = min(rest, WT) * Q4_REC;
+          mbar_arrive_expect_tx(&full[warp][s_in], bytes);
+          bulk_load(ring + s_in * STAGE_BYTES, src, bytes, &full[warp][s_in]);
+        }
+        filled |= 1u << s_in;
+        odd ^= 1u << s_in;
+        s_in = s_in + 1 == STAGES ? 0 : s_in + 1;
+        ++in_flight;
+      }
+      rest -= TILE;
+      src += TILE * Q4_REC;
+      --left;
+      if (--run == 0) {
+        ahead.i = ahead.nt - 1;
+        tile_next(ahead, s_pre, lens, B, cap, Hkv);
+      }
     }
   };
   fill();
 
   for (int64_t tt = t0; tt < t1;) {
-    // ---- one (sequence, KV head): tiles at.i .. of it in this CTA's range
+    // ---- one (sequence, KV head): its tiles in this CTA's range
     const int b = at.b, g = at.g;
-    const int64_t seg_end = min(t1, tt + (at.nt - at.i));
+    const int tiles = int(min(t1 - tt, int64_t(at.nt - at.i)));
+    tt += tiles;
     Q4State<NT> st;
     q4_init<NT>(st, q + (int64_t(b) * Hkv + g) * G * 128, G, scale_log2);
-    float* lg = LOGITS ? logits + (int64_t(b) * Hkv + g) * cap * G : nullptr;
-    for (; tt < seg_end; ++tt) {
-      const int n = count(at);
-      if (n > 0) {
-        const int s = used % STAGES;
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[warp][s], (used / STAGES) & 1));
-        const int64_t key0 = int64_t(at.i) * TILE + warp * WT;
-#pragma unroll
-        for (int h = 0; h < WT / 16; ++h) {
-          const int nv = n - 16 * h;
-          if (nv <= 0) break;
-          q4_step<NT>(st, ring + s * STAGE_BYTES + h * 16 * Q4_REC, nv, [&](int nt, const float* x) {
-            if constexpr (LOGITS) {
-              const int h0 = nt * 8 + 2 * t;
-              float* r = lg + (key0 + 16 * h + gid) * G + h0;
-              if (h0 + 1 < G) {
-                if (gid < nv) *reinterpret_cast<float2*>(r) = make_float2(x[0], x[1]);
-                if (gid + 8 < nv) *reinterpret_cast<float2*>(r + 8 * G) = make_float2(x[2], x[3]);
-              } else if (h0 < G) {
-                if (gid < nv) r[0] = x[0];
-                if (gid + 8 < nv) r[8 * G] = x[2];
-              }
-            }
-          });
+    int n = at.len - at.i * TILE - warp * WT;  // tokens from this warp's part on
+    float* lg = LOGITS ? logits + ((int64_t(b) * Hkv + g) * cap + at.i * TILE + warp * WT + gid) * G + 2 * t
+                       : nullptr;
+    for (int i = 0; i < tiles && n > 0; ++i, n -= TILE) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[warp][s_out], (ph >> s_out) & 1));
+      ph ^= 1u << s_out;
+      const uint8_t* rec = ring + s_out * STAGE_BYTES;
+      auto put = [&](int h, int nt, const float (&x)[4]) {
+        const int h0 = nt * 8 + 2 * t, nv = n - 16 * h;
+        float* r = lg + 16 * h * G + nt * 8;
+        if (h0 + 1 < G) {
+          if (gid < nv) *reinterpret_cast<float2*>(r) = make_float2(x[0], x[1]);
+          if (gid + 8 < nv) *reinterpret_cast<float2*>(r + 8 * G) = make_float2(x[2], x[3]);
+        } else if (h0 < G) {
+          if (gid < nv) r[0] = x[0];
+          if (gid + 8 < nv) r[8 * G] = x[2];
         }
-        ++used;
-        __syncwarp();  // every lane has read the stage before it is filled again
-        fill();
-      }
-      tile_next(at, s_pre, lens, B, cap, Hkv);
+      };
+      if (n >= WT)
+        q4_step<NT, WT / 16, true, LOGITS>(st, rec, WT, put);
+      else
+        q4_step<NT, WT / 16, false, LOGITS>(st, rec, n, put);
+      if (LOGITS) lg += TILE * G;
+      s_out = s_out + 1 == STAGES ? 0 : s_out + 1;
+      --in_flight;
+      __syncwarp();  // every lane has read the stage before it is filled again
+      if (ok) fill();
     }
+    at.i = at.nt - 1;
+    tile_next(at, s_pre, lens, B, cap, Hkv);
     // ---- join the warps and write the partial
     q4_put<NT>(st, join.m[warp], join.l[warp], join.o[warp]);
     __syncthreads();
@@ -251,30 +264,34 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
     }
     __syncthreads();
   }
-  // a copy that was issued but never attended (a wait ran out) lands before exit
-  if (lane == 0)
+  // after a wait that ran out: every copy that was issued lands before exit
+  if (!ok && lane == 0)
     for (int s = 0; s < STAGES; ++s)
-      drain_phase(&full[warp][s], issued > s ? (issued - 1 - s) / STAGES + 1 : 0);
+      if ((filled >> s) & 1)
+        mbar_wait_budget(&full[warp][s], ((odd >> s) & 1) ^ 1, kDrainBudgetCycles);
 }
 
-// grid (Hkv * G, B), 128 threads: the partials of (b, head) -> o, lse
-__global__ void __launch_bounds__(128)
+// grid (Hkv * G, B): the partials of (b, head) -> o, lse.  Each of MW warps
+// takes every MW-th partial, four dims per lane.
+constexpr int MW = NW;
+__global__ void __launch_bounds__(MW * 32)
     decode_attn_q4_merge(const float2* __restrict__ part, const float* __restrict__ part_o,
                          const __grid_constant__ Q4Lens lens, int B, int64_t cap, int Hkv, int G,
                          int n_ctas, __nv_bfloat16* __restrict__ o, float* __restrict__ lse,
                          float* __restrict__ lse2) {
   __shared__ int s_pre[kQ4MaxBatch + 1];
   __shared__ int s_sum[NW];
-  __shared__ float s_red[NW];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int h = blockIdx.x % G, g = blockIdx.x / G, b = blockIdx.y, tid = threadIdx.x;
+  __shared__ float s_m[MW], s_l[MW];
+  __shared__ __align__(16) float s_o[MW][128];
+  const int h = blockIdx.x % G, g = blockIdx.x / G, b = blockIdx.y, lane = lane_id(), warp = warp_id();
   tile_prefix(lens, B, cap, s_pre, s_sum);
   const int64_t total = int64_t(s_pre[B]) * Hkv;
   const int nt = s_pre[b + 1] - s_pre[b];
   const int64_t head = int64_t(b) * Hkv * G + g * G + h;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (nt == 0) {  // an empty context
-    o[head * 128 + tid] = __float2bfloat16_rn(0.f);
-    if (tid == 0) {
+    o[head * 128 + threadIdx.x] = __float2bfloat16_rn(0.f);
+    if (threadIdx.x == 0) {
       if (lse != nullptr) lse[head] = -INFINITY;
       if (lse2 != nullptr) lse2[head] = -INFINITY;
     }
@@ -287,24 +304,57 @@ __global__ void __launch_bounds__(128)
   const int64_t c0 = cta_of(S), c1 = cta_of(S + nt - 1);
   const int64_t base = (c0 + int64_t(b) * Hkv + g) * G + h;
   const int n = int(c1 - c0 + 1);
-  float M = -INFINITY;
-  for (int i = tid; i < n; i += 128) M = fmaxf(M, part[base + int64_t(i) * G].x);
+  // running maximum, sum and output of this warp's partials, eight at a time
+  float M = -INFINITY, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int U = 8;
+  for (int i0 = warp; i0 < n; i0 += U * MW) {
+    float2 p[U];
+    float4 v[U];
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  if (lane_id() == 0) s_red[warp_id()] = M;
-  __syncthreads();
-  M = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
-  float L = 0.f, acc = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) {
-    const float2 p = part[base + int64_t(i) * G];
-    const float w = p.x == -INFINITY ? 0.f : fast_exp2(p.x - M);
-    L += p.y * w;
-    acc += part_o[(base + int64_t(i) * G) * 128 + tid] * w;
+    for (int u = 0; u < U; ++u) {
+      const int64_t at = base + int64_t(min(i0 + u * MW, n - 1)) * G;
+      p[u] = __ldcg(part + at);
+      v[u] = __ldcg(reinterpret_cast<const float4*>(part_o + at * 128) + lane);
+      if (i0 + u * MW >= n) p[u] = make_float2(-INFINITY, 0.f);
+    }
+    float m = M;
+#pragma unroll
+    for (int u = 0; u < U; ++u) m = fmaxf(m, p[u].x);
+    const float keep = M == -INFINITY ? 0.f : fast_exp2(M - m);
+    M = m;
+    L *= keep;
+    acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float w = p[u].x == -INFINITY ? 0.f : fast_exp2(p[u].x - M);
+      if (i0 + u * MW < n) {
+        L += p[u].y * w;
+        acc.x += v[u].x * w;
+        acc.y += v[u].y * w;
+        acc.z += v[u].z * w;
+        acc.w += v[u].w * w;
+      }
+    }
   }
-  o[head * 128 + tid] = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
-  if (tid == 0) {
-    const float l2 = L == 0.f ? -INFINITY : M + __log2f(L);
+  *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = acc;
+  if (lane == 0) {
+    s_m[warp] = M;
+    s_l[warp] = L;
+  }
+  __syncthreads();
+  float m = -INFINITY, l = 0.f, a = 0.f;
+#pragma unroll
+  for (int w = 0; w < MW; ++w) m = fmaxf(m, s_m[w]);
+#pragma unroll
+  for (int w = 0; w < MW; ++w) {
+    const float f = s_m[w] == -INFINITY ? 0.f : fast_exp2(s_m[w] - m);
+    l += s_l[w] * f;
+    a += s_o[w][threadIdx.x] * f;
+  }
+  o[head * 128 + threadIdx.x] = __float2bfloat16_rn(l == 0.f ? 0.f : a / l);
+  if (threadIdx.x == 0) {
+    const float l2 = l == 0.f ? -INFINITY : m + __log2f(l);
     if (lse != nullptr) lse[head] = l2 * kLn2;
     if (lse2 != nullptr) lse2[head] = l2;
   }
@@ -330,7 +380,7 @@ __global__ void __launch_bounds__(NW * 32)
   __shared__ uint64_t full[NW][SST];
   // this CTA's joined state, read by the cluster's first CTA
   __shared__ float cM[NT * 8], cL[NT * 8];
-  __shared__ float cO[NT * 8][128];
+  __shared__ __align__(16) float cO[NT * 8][128];
   extern __shared__ uint8_t dsmem_raw[];
   uint8_t* dsmem = dsmem_raw + ((16u - (smem_u32(dsmem_raw) & 15u)) & 15u);
   JoinBuf<NT>& join = *reinterpret_cast<JoinBuf<NT>*>(dsmem + NW * SST * SSTAGE_BYTES);
@@ -385,7 +435,12 @@ __global__ void __launch_bounds__(NW * 32)
   while (used < issued) {
     const int s = used % SST;
     ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[warp][s], (used / SST) & 1));
-    q4_step<NT>(st, ring + s * SSTAGE_BYTES, (counts >> (8 * s)) & 0xFF, [](int, const float*) {});
+    const int nv = (counts >> (8 * s)) & 0xFF;
+    const auto none = [](int, int, const float (&)[4]) {};
+    if (nv == 16)
+      q4_step<NT, 1, true, false>(st, ring + s * SSTAGE_BYTES, nv, none);
+    else
+      q4_step<NT, 1, false, false>(st, ring + s * SSTAGE_BYTES, nv, none);
     ++used;
     __syncwarp();
     fill();
@@ -471,7 +526,7 @@ cudaError_t launch_attn_g(const Q4AttnArgs& a, cudaStream_t st) {
   // for the whole grid before they read a partial
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(a.Hkv) * G, unsigned(a.B));
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(MW * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

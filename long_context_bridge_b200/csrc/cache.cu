@@ -24,6 +24,19 @@ namespace {
 constexpr int TOK = 4;       // tokens per warp
 constexpr int CW_WARPS = 4;  // warps per CTA
 
+// s / cap for s < 2^31: mul = floor(2^shift / cap) + 1 with shift = 31 +
+// ceil(log2 cap) is 2^shift / cap (1 + e), 0 < e <= 2^-31, so s * mul / 2^shift
+// exceeds s / cap by less than 1 / cap and has the same whole part.
+struct SlotDiv {
+  uint64_t mul;
+  uint32_t shift, cap;
+};
+SlotDiv slot_div(int64_t cap) {
+  uint32_t l = 0;
+  while ((int64_t(1) << l) < cap) ++l;
+  return SlotDiv{(uint64_t(1) << (31 + l)) / uint64_t(cap) + 1, 31 + l, uint32_t(cap)};
+}
+
 // The cache slot of token i, or -1 for none (a slot outside [0, n_slots) is
 // reported and skipped like -1).
 __device__ __forceinline__ int64_t token_slot(const int32_t* __restrict__ slot, int64_t first,
@@ -34,6 +47,13 @@ __device__ __forceinline__ int64_t token_slot(const int32_t* __restrict__ slot, 
   if (s >= 0 && s < n_slots) return s;
   if (s != -1) set_dev_status(DEV_BAD_INDEX);
   return -1;
+}
+
+// Record of slot s (s < 2^31): s / cap by the precomputed reciprocal.
+__device__ __forceinline__ int64_t record_of(int64_t s, const SlotDiv& d, int h, int Hkv) {
+  const uint32_t b = uint32_t((uint64_t(uint32_t(s)) * d.mul) >> d.shift);
+  const uint32_t p = uint32_t(s) - b * d.cap;
+  return (int64_t(b) * Hkv + h) * d.cap + p;
 }
 
 // largest |x| of a lane's eight bf16 values, as bf16 bits (a NaN ranks above
@@ -69,7 +89,7 @@ __device__ __forceinline__ int stored_word(bool v, int g, int t) {
 __global__ void __launch_bounds__(CW_WARPS * 32)
     cache_write_q4(const __nv_bfloat16* __restrict__ K, const __nv_bfloat16* __restrict__ V,
                    int64_t ldk, int64_t ldv, const int32_t* __restrict__ slot, int64_t first,
-                   int64_t n, uint8_t* __restrict__ cache, int64_t cap, int64_t n_slots, int Hkv) {
+                   int64_t n, uint8_t* __restrict__ cache, SlotDiv div, int64_t n_slots, int Hkv) {
   const int h = blockIdx.y, lane = lane_id();
   const bool is_v = lane >= 16;
   const int m = lane & 15, g = m >> 2, t = m & 3;
@@ -98,8 +118,7 @@ __global__ void __launch_bounds__(CW_WARPS * 32)
     // the pair of groups (g, g ^ 1): the even one stores both scales
     const uint32_t s2 = __shfl_xor_sync(0xffffffffu, sc.bits, 4);
     if (at[u] < 0) continue;
-    const int64_t b = at[u] / cap, p = at[u] - b * cap;
-    uint8_t* rec = cache + ((b * Hkv + h) * cap + p) * Q4_REC;
+    uint8_t* rec = cache + record_of(at[u], div, h, Hkv) * Q4_REC;
     reinterpret_cast<uint32_t*>(rec + (is_v ? Q4_V : Q4_K))[stored_word(is_v, g, t)] = w;
     if (t == 0 && (g & 1) == 0)
       reinterpret_cast<uint32_t*>(rec + (is_v ? Q4_VS : Q4_KS))[g >> 1] = sc.bits | (s2 << 16);
@@ -109,7 +128,7 @@ __global__ void __launch_bounds__(CW_WARPS * 32)
 __global__ void __launch_bounds__(CW_WARPS * 32)
     cache_read_q4(const uint8_t* __restrict__ cache, const int32_t* __restrict__ slot,
                   int64_t first, int64_t n, __nv_bfloat16* __restrict__ K,
-                  __nv_bfloat16* __restrict__ V, int64_t ldk, int64_t ldv, int64_t cap,
+                  __nv_bfloat16* __restrict__ V, int64_t ldk, int64_t ldv, SlotDiv div,
                   int64_t n_slots, int Hkv) {
   const int h = blockIdx.y, lane = lane_id();
   const bool is_v = lane >= 16;
@@ -125,8 +144,7 @@ __global__ void __launch_bounds__(CW_WARPS * 32)
     at[u] = token_slot(slot, first, i0 + u, n, n_slots);
     w[u] = s[u] = 0;
     if (at[u] >= 0) {
-      const int64_t b = at[u] / cap, p = at[u] - b * cap;
-      const uint8_t* rec = cache + ((b * Hkv + h) * cap + p) * Q4_REC;
+      const uint8_t* rec = cache + record_of(at[u], div, h, Hkv) * Q4_REC;
       w[u] = __ldg(reinterpret_cast<const uint32_t*>(rec + (is_v ? Q4_V : Q4_K)) +
                    stored_word(is_v, g, t));
       s[u] = __ldg(reinterpret_cast<const uint16_t*>(rec + (is_v ? Q4_VS : Q4_KS)) + g);
@@ -137,13 +155,21 @@ __global__ void __launch_bounds__(CW_WARPS * 32)
     const uint32_t wv = v_trade(w[u], g);  // its own inverse
     const uint32_t x = is_v ? wv : w[u];
     if (at[u] < 0) continue;
-    const float sc = __uint_as_float(s[u] << 16);
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o[i] = pack_bf16x2(q4_value(x >> (8 * i)) * sc, q4_value(x >> (8 * i + 4)) * sc);
-    stg_stream(dst + (i0 + u) * ld, make_uint4(o[0], o[1], o[2], o[3]));
+    stg_stream(dst + (i0 + u) * ld, q4_values8(x, s[u]));
   }
+}
+
+// x / s rounded to nearest, for r = the correctly rounded 1 / s: one step of
+// Markstein's correction (P. Markstein, IBM Journal of Research and Development
+// 34, 1990: q' = q + r (x - s q) is the correctly rounded quotient), whose
+// remainder is exact as long as it is not subnormal.  A row pair whose largest
+// |x| lies below 2^-60 takes the plain division; above, s >= 2^-69, and an x
+// whose remainder could be subnormal (|x| < 2^-101) has a quotient below 2^-32,
+// which every rounding sends to the code 0.
+constexpr uint32_t kPlainBelow = (127 - 60) << 7;
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+  const float q = __fmul_rn(x, r);
+  return copysignf(__fmaf_rn(__fmaf_rn(-s, q, x), r, q), x);  // -0 stays -0
 }
 
 // e4m3 of one fp32 quotient pair: nearest, ties to the even code, saturated
@@ -183,7 +209,12 @@ __global__ void __launch_bounds__(CW_WARPS * 32)
     float x[8];
     unpack8(v[u], x);
     uint32_t c[2] = {0, 0};
-    if (finite) {
+    if (a >= kPlainBelow && finite) {
+      const float r = __frcp_rn(s);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        c[i >> 1] |= e4m3x2(quotient(x[2 * i], s, r), quotient(x[2 * i + 1], s, r)) << (16 * (i & 1));
+    } else if (finite) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         c[i >> 1] |= e4m3x2(x[2 * i] / s, x[2 * i + 1] / s) << (16 * (i & 1));
@@ -256,7 +287,7 @@ cudaError_t launch_cache_write(const CacheRowsArgs& a, cudaStream_t st) {
   const auto* V = reinterpret_cast<const __nv_bfloat16*>(a.V);
   if (a.cache != nullptr)
     cache_write_q4<<<cache_grid(a), CW_WARPS * 32, 0, st>>>(
-        K, V, a.ldk, a.ldv, a.slot, a.first, a.n, a.cache, a.cap, a.n_slots, a.Hkv);
+        K, V, a.ldk, a.ldv, a.slot, a.first, a.n, a.cache, slot_div(a.cap), a.n_slots, a.Hkv);
   else
     cache_write_fp8<<<cache_grid(a), CW_WARPS * 32, 0, st>>>(
         K, V, a.ldk, a.ldv, a.slot, a.first, a.n, a.Kc, a.Vc, const_cast<float*>(a.ks), a.n_slots,
@@ -270,7 +301,8 @@ cudaError_t launch_cache_read(const CacheRowsArgs& a, cudaStream_t st) {
   auto* V = reinterpret_cast<__nv_bfloat16*>(const_cast<void*>(a.V));
   if (a.cache != nullptr)
     cache_read_q4<<<cache_grid(a), CW_WARPS * 32, 0, st>>>(a.cache, a.slot, a.first, a.n, K, V,
-                                                           a.ldk, a.ldv, a.cap, a.n_slots, a.Hkv);
+                                                           a.ldk, a.ldv, slot_div(a.cap), a.n_slots,
+                                                           a.Hkv);
   else
     cache_read_fp8<<<cache_grid(a), CW_WARPS * 32, 0, st>>>(a.Kc, a.Vc, a.ks, a.vs, a.slot,
                                                             a.first, a.n, K, V, a.ldk, a.ldv,

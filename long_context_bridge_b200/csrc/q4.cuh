@@ -39,56 +39,75 @@ __device__ __forceinline__ void stg_stream(void* p, const uint4& v) {
 }
 
 struct Q4Scale {
-  float inv;      // 1 / scale
+  float inv;      // 1 / scale, within 2^-22 of it
   uint32_t bits;  // the scale's bf16 bits
   bool finite;
 };
 
-// scale of a group whose largest |x| has the bf16 bits a
+// Scale of a group whose largest |x| has the bf16 bits a.  amax * (1 / 7) is
+// within 2^-22 of amax / 7, which lies at least 2^-12 away (relative) from
+// every tie between two bf16 values (14 * the distance, in units of its ulp, is
+// a non-zero whole number), so both round to the same scale.
 __device__ __forceinline__ Q4Scale q4_scale(uint32_t a) {
   Q4Scale s;
   s.finite = a < 0x7F80u;
-  const float q = fmaxf(__uint_as_float(a << 16) / 7.f, __uint_as_float(7u << 23));  // 2^-120
+  const float q = fmaxf(__uint_as_float(a << 16) * (1.f / 7.f), __uint_as_float(7u << 23));  // 2^-120
   const __nv_bfloat16 b = __float2bfloat16_rn(q);
   s.bits = s.finite ? uint32_t(*reinterpret_cast<const uint16_t*>(&b)) : 0x7FC0u;
-  s.inv = 1.f / __uint_as_float(s.bits << 16);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.inv) : "f"(__uint_as_float(s.bits << 16)));
   return s;
 }
 
-// Eight codes as one word, element n in nibble n.  x / s is formed as x * (1 /
-// s), within 2^-20 of the quotient (|x / s| < 7.04).  x and s have 8
-// significant bits each, so a quotient is a tie k + 1/2 exactly or at least
-// 1 / 510 away from it: snapping to multiples of 2^-11 puts every tie back on
-// itself and moves no other quotient across one.  Adding 1.5 * 2^23 + 8 then
-// rounds to an integer (ties to even) and leaves code + 8 in the low bits.
+// Eight codes as one word, element n in nibble n.  x * inv is within 2^-19 of
+// x / s (|x / s| < 7.04).  x and s have 8 significant bits each, so a quotient
+// is a tie k + 1/2 exactly or at least 1 / 510 away from it: forming x * inv +
+// 6144 (ulp 2^-11) puts every tie back on itself and moves no other quotient
+// across one.  Adding 12582920 - 6144 then rounds to an integer (ulp 1, ties to
+// even) and leaves code + 8 in the low bits.
 __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], const Q4Scale& s) {
-  constexpr float kSnap = 6144.f;                // 1.5 * 2^12: ulp 2^-11
-  constexpr float kRound = 12582912.f + 8.f;     // ulp 1
-  constexpr uint32_t kBase = 0x4B400000u;        // bits of 12582912
-  uint32_t w = 0;
+  constexpr uint32_t kBase = 0x4B400000u;  // bits of 12582912
+  uint32_t w = 0u - (kBase + (kBase << 4) + (kBase << 8));  // further shifts leave the word
 #pragma unroll
   for (int n = 0; n < 8; ++n) {
-    const float q = __fadd_rn(__fadd_rn(__fmul_rn(x[n], s.inv), kSnap), -kSnap);
-    w += (__float_as_uint(__fadd_rn(q, kRound)) - kBase) << (4 * n);
+    const float q = __fadd_rn(__fmaf_rn(x[n], s.inv, 6144.f), 12582920.f - 6144.f);
+    w += __float_as_uint(q) << (4 * n);
   }
   return s.finite ? w : 0x88888888u;
 }
 
-// (low nibble - 8) as fp32
-__device__ __forceinline__ float q4_value(uint32_t w) {
-  return __uint_as_float(0x4B000000u | (w & 15u)) - 8388616.f;
+// Eight values (nibble - 8) * scale rounded to bf16, in order.  bf16 bits
+// 0x4300 | u = 128 + u; nibbles j and j + 4 are handled as a pair.
+__device__ __forceinline__ uint4 q4_values8(uint32_t w, uint32_t scale_bits) {
+  const __nv_bfloat162 k136 = __float2bfloat162_rn(-136.f);
+  const uint32_t s2 = scale_bits * 0x00010001u;
+  uint32_t p[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t u = ((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u;
+    const __nv_bfloat162 v = __hmul2(__hadd2(*reinterpret_cast<const __nv_bfloat162*>(&u), k136),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&s2));
+    p[j] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
+                    __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632));
 }
 
 // ---------------------------------------------------------------------------
 // attending
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+// D = A B + C
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1, float c0,
+                                              float c1, float c2, float c3) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  mma_f16_16816(c, a0, a1, a2, a3, b0, b1, c[0], c[1], c[2], c[3]);
 }
 
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
@@ -130,17 +149,18 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // the running maximum - 10 and moved only when some x passes it by 14, so p
 // lies below 2^14 and the accumulators are rarely rescaled.
 //
-// O^T += V^T P^T: P is rounded to f16 (2^-12 relative; below 2^-24 of the
-// running maximum by an absolute 2^-35 of it), transposed by movmatrix,
-// multiplied by each group's V scale relative to `r2` (the power of two at or
-// below the largest V scale met so far) and rounded to f16 once more; V's codes
-// are exact in f16.
+// O^T += V^T P^T: P times each group's V scale relative to `r2` (the power of
+// two at or below the largest V scale met so far) is rounded to f16 (2^-11
+// relative; below 2^-24 of the running maximum an absolute 2^-35 of it) where
+// the softmax has it, [key][head], and transposed by movmatrix into the B
+// fragment; V's codes are exact in f16.
 template <int NT>
 struct Q4State {
   uint32_t qf[NT][4][2][2];  // [group][MMA][register]
   float q8[NT][4][2];        // -8 * sum of the group's q * 2^-24, heads 2t / 2t+1
-  float f[NT][2];            // logit (base 2) = f * scaled sum
+  float f[NT][2];            // logit (base 2) = f * scaled sum (f > 0)
   float ref[NT][2], l[NT][2];
+  float top[NT][2];          // (ref + 14) / f: a scaled sum above it moves ref
   float o[NT][8][4];
   uint32_t r_bits;           // bf16 bits of r2
   float r_inv;               // 1 / r2
@@ -208,7 +228,7 @@ __device__ __forceinline__ void q4_init(Q4State<NT>& st, const __nv_bfloat16* __
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       st.f[nt][i] = (scale_log2 * 16777216.f) * __shfl_sync(0xffffffffu, back, 4 * (2 * t + i));
-      st.ref[nt][i] = -INFINITY;
+      st.ref[nt][i] = st.top[nt][i] = -INFINITY;
       st.l[nt][i] = 0.f;
     }
 #pragma unroll
@@ -219,20 +239,24 @@ __device__ __forceinline__ void q4_init(Q4State<NT>& st, const __nv_bfloat16* __
 }
 
 // Moves the softmax references up to (maximum - 10) and r2 up to the largest
-// finite V scale's power of two; rescales what was accumulated.
-template <int NT>
-__device__ __forceinline__ void q4_raise(Q4State<NT>& st, const float (&x)[NT][4],
-                                      const uint2 (&vs)[4]) {
+// finite V scale's power of two; rescales what was accumulated.  s: the scaled
+// sums of 16 H keys; vs: V scales of the lane's 2 H keys.
+template <int NT, int H>
+__device__ __forceinline__ void q4_raise(Q4State<NT>& st, const float (&s)[H][NT][4],
+                                         const uint2 (&vs)[H][2]) {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float mx = fmaxf(x[nt][i], x[nt][i + 2]);
+      float mx = fmaxf(s[0][nt][i], s[0][nt][i + 2]);
+#pragma unroll
+      for (int h = 1; h < H; ++h) mx = fmaxf(mx, fmaxf(s[h][nt][i], s[h][nt][i + 2]));
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-      const float old = st.ref[nt][i], up = fmaxf(old, mx - 10.f);
+      const float old = st.ref[nt][i], up = fmaxf(old, mx * st.f[nt][i] - 10.f);
       const float al = old == up ? 1.f : fast_exp2(old - up);
       st.ref[nt][i] = up;
+      st.top[nt][i] = (up + 14.f) / st.f[nt][i];
       st.l[nt][i] *= al;
 #pragma unroll
       for (int d = 0; d < 8; ++d) {
@@ -242,11 +266,14 @@ __device__ __forceinline__ void q4_raise(Q4State<NT>& st, const float (&x)[NT][4
     }
   uint32_t r = 0;
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const uint32_t b[4] = {vs[u].x & 0xFFFFu, vs[u].x >> 16, vs[u].y & 0xFFFFu, vs[u].y >> 16};
+  for (int h = 0; h < H; ++h)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r = max(r, b[i] < 0x7F80u ? b[i] : 0u);
-  }
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t b[4] = {vs[h][u].x & 0xFFFFu, vs[h][u].x >> 16, vs[h][u].y & 0xFFFFu,
+                             vs[h][u].y >> 16};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r = max(r, b[i] < 0x7F80u ? b[i] : 0u);
+    }
   r = __reduce_max_sync(0xffffffffu, r) & 0x7F80u;
   if (r > st.r_bits) {
     const float al = q4_pow2_bits(st.r_bits) * q4_inv_pow2(r);
@@ -261,122 +288,133 @@ __device__ __forceinline__ void q4_raise(Q4State<NT>& st, const float (&x)[NT][4
   }
 }
 
-// Attends the first nv (1 .. 16) of the 16 records at `rec` (shared memory).
-// on_logits(nt, x): the lane's base-2 logits {key gid: heads 2t, 2t+1; key
-// gid + 8: the same}, -inf from key nv on.
-template <int NT, class F>
+// Attends the first nv (1 .. 16 H) of the 16 H records at `rec` (shared
+// memory); FULL: nv = 16 H.  on_logits(h, nt, x): the lane's base-2 logits of
+// keys 16 h + gid (heads 2t, 2t + 1) and 16 h + gid + 8 (the same heads), -inf
+// from key nv on.
+template <int NT, int H, bool FULL, bool LOGITS, class F>
 __device__ __forceinline__ void q4_step(Q4State<NT>& st, const uint8_t* rec, int nv, F&& on_logits) {
   const int lane = lane_id(), gid = lane >> 2, t = lane & 3;
-  // ---- S^T
-  const uint8_t* ra = rec + gid * Q4_REC;
-  const uint8_t* rb = ra + 8 * Q4_REC;
-  const uint4 ka = *reinterpret_cast<const uint4*>(ra + Q4_K + 16 * t);
-  const uint4 kb = *reinterpret_cast<const uint4*>(rb + Q4_K + 16 * t);
-  const uint2 sa = *reinterpret_cast<const uint2*>(ra + Q4_KS);
-  const uint2 sb = *reinterpret_cast<const uint2*>(rb + Q4_KS);
-  // V rows of the lane's four keys (B-fragment order) and their scales
-  uint2 vw[4], vs[4];
+  float s[H][NT][4];
+  uint2 vs[H][2];  // V scales of keys gid, gid + 8
+  // ---- S^T: per group of dims an fp32 sum, times the key's K scale
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int key = 2 * t + (u & 1) + 8 * (u >> 1);
-    const uint8_t* rv = rec + key * Q4_REC;
-    vw[u] = *reinterpret_cast<const uint2*>(rv + Q4_V + 8 * gid);
-    vs[u] = *reinterpret_cast<const uint2*>(rv + Q4_VS);
-    if (key >= nv) vs[u] = make_uint2(0, 0);
-  }
-  float x[NT][4];
-  const uint32_t kw0[4] = {ka.x, ka.y, ka.z, ka.w}, kw1[4] = {kb.x, kb.y, kb.z, kb.w};
-  const float ks0[4] = {bf16lo(sa.x), bf16hi(sa.x), bf16lo(sa.y), bf16hi(sa.y)};
-  const float ks1[4] = {bf16lo(sb.x), bf16hi(sb.x), bf16lo(sb.y), bf16hi(sb.y)};
+  for (int h = 0; h < H; ++h) {
+    const uint8_t* ra = rec + (16 * h + gid) * Q4_REC;
+    const uint8_t* rb = ra + 8 * Q4_REC;
+    const uint4 ka = *reinterpret_cast<const uint4*>(ra + Q4_K + 16 * t);
+    const uint4 kb = *reinterpret_cast<const uint4*>(rb + Q4_K + 16 * t);
+    const uint4 sa = *reinterpret_cast<const uint4*>(ra + Q4_KS);  // K scales, V scales
+    const uint4 sb = *reinterpret_cast<const uint4*>(rb + Q4_KS);
+    vs[h][0] = make_uint2(sa.z, sa.w);
+    vs[h][1] = make_uint2(sb.z, sb.w);
+    if (!FULL) {
+      if (16 * h + gid >= nv) vs[h][0] = make_uint2(0, 0);
+      if (16 * h + gid + 8 >= nv) vs[h][1] = make_uint2(0, 0);
+    }
+    const uint32_t kw0[4] = {ka.x, ka.y, ka.z, ka.w}, kw1[4] = {kb.x, kb.y, kb.z, kb.w};
+    const float ks0[4] = {bf16lo(sa.x), bf16hi(sa.x), bf16lo(sa.y), bf16hi(sa.y)};
+    const float ks1[4] = {bf16lo(sb.x), bf16hi(sb.x), bf16lo(sb.y), bf16hi(sb.y)};
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const uint32_t w0 = kw0[g], w1 = kw1[g], v0 = w0 >> 8, v1 = w1 >> 8;
+    for (int g = 0; g < 4; ++g) {
+      const uint32_t w0 = kw0[g], w1 = kw1[g], v0 = w0 >> 8, v1 = w1 >> 8;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float c[4] = {st.q8[nt][g][0], st.q8[nt][g][1], st.q8[nt][g][0], st.q8[nt][g][1]};
-      mma_f16_16816(c, w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u,
-                    st.qf[nt][g][0][0], st.qf[nt][g][0][1]);
-      mma_f16_16816(c, v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u,
-                    st.qf[nt][g][1][0], st.qf[nt][g][1][1]);
+      for (int nt = 0; nt < NT; ++nt) {
+        float c[4];
+        mma_f16_16816(c, w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u,
+                      st.qf[nt][g][0][0], st.qf[nt][g][0][1], st.q8[nt][g][0], st.q8[nt][g][1],
+                      st.q8[nt][g][0], st.q8[nt][g][1]);
+        mma_f16_16816(c, v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u,
+                      st.qf[nt][g][1][0], st.qf[nt][g][1][1]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float s = i < 2 ? ks0[g] : ks1[g];
-        x[nt][i] = g == 0 ? c[i] * s : fmaf(c[i], s, x[nt][i]);
+        for (int i = 0; i < 4; ++i) {
+          const float k = i < 2 ? ks0[g] : ks1[g];
+          s[h][nt][i] = g == 0 ? c[i] * k : fmaf(c[i], k, s[h][nt][i]);
+        }
       }
     }
   }
-  // ---- logits, and whether a reference has to move
+  // ---- does a reference have to move?
   bool raise = false;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[nt][i] *= st.f[nt][i & 1];
-      if (gid + 8 * (i >> 1) >= nv) x[nt][i] = -INFINITY;
-    }
-    on_logits(nt, x[nt]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) raise |= x[nt][i] > st.ref[nt][i & 1] + 14.f;
-  }
   uint32_t vmax = 0;
 #pragma unroll
-  for (int u = 0; u < 4; ++u) vmax = __vmaxu2(vmax, __vmaxu2(vs[u].x, vs[u].y));
+  for (int h = 0; h < H; ++h) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (!FULL) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (16 * h + gid + 8 * (i >> 1) >= nv) s[h][nt][i] = -INFINITY;
+      }
+      if (LOGITS) {
+        const float x[4] = {s[h][nt][0] * st.f[nt][0], s[h][nt][1] * st.f[nt][1],
+                            s[h][nt][2] * st.f[nt][0], s[h][nt][3] * st.f[nt][1]};
+        on_logits(h, nt, x);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) raise |= s[h][nt][i] > st.top[nt][i & 1];
+    }
+    vmax = __vmaxu2(vmax, __vmaxu2(__vmaxu2(vs[h][0].x, vs[h][0].y), __vmaxu2(vs[h][1].x, vs[h][1].y)));
+  }
   const uint32_t top = (st.r_bits | 0x7Fu) * 0x00010001u;
   raise |= __vmaxu2(vmax, top) != top;
-  if (__any_sync(0xffffffffu, raise)) q4_raise<NT>(st, x, vs);
-  // ---- P: [key][head] -> [head][keys], then times V's scales per group
-  const float vsc[4][4] = {
-      {bf16lo(vs[0].x), bf16hi(vs[0].x), bf16lo(vs[0].y), bf16hi(vs[0].y)},
-      {bf16lo(vs[1].x), bf16hi(vs[1].x), bf16lo(vs[1].y), bf16hi(vs[1].y)},
-      {bf16lo(vs[2].x), bf16hi(vs[2].x), bf16lo(vs[2].y), bf16hi(vs[2].y)},
-      {bf16lo(vs[3].x), bf16hi(vs[3].x), bf16lo(vs[3].y), bf16hi(vs[3].y)}};
-  uint32_t pb[NT][4][2];
+  if (__any_sync(0xffffffffu, raise)) q4_raise<NT, H>(st, s, vs);
+  float sub[NT][2];  // no key yet: ref = -inf, every logit = -inf, p = 0
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    float p[4];
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // no key yet: ref = -inf, every x = -inf, p = 0
-      const float ref = st.ref[nt][i & 1];
-      p[i] = fast_exp2(x[nt][i] - (ref == -INFINITY ? 0.f : ref));
-      st.l[nt][i & 1] += p[i];
-    }
-    const uint32_t t0 = movmatrix_trans(pack_h2(p[0], p[1]));
-    const uint32_t t1 = movmatrix_trans(pack_h2(p[2], p[3]));
-    const float2 p01 = __half22float2(*reinterpret_cast<const __half2*>(&t0));
-    const float2 p89 = __half22float2(*reinterpret_cast<const __half2*>(&t1));
-    const float q0 = p01.x * st.r_inv, q1 = p01.y * st.r_inv;
-    const float q2 = p89.x * st.r_inv, q3 = p89.y * st.r_inv;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      pb[nt][g][0] = pack_h2(q0 * vsc[0][g], q1 * vsc[1][g]);
-      pb[nt][g][1] = pack_h2(q2 * vsc[2][g], q3 * vsc[3][g]);
-    }
-  }
-  // ---- O^T: per group two 16-dim tiles; nibble j of a half word = tile j / 2,
-  // row gid + 8 (j % 2).  f16 bits 0x6400 | u = 1024 + u, 0x6400 | u << 4 =
-  // 1024 + 16 u
+    for (int i = 0; i < 2; ++i) sub[nt][i] = !FULL && st.ref[nt][i] == -INFINITY ? 0.f : -st.ref[nt][i];
   const __half2 k1032 = __float2half2_rn(-1032.f), k16th = __float2half2_rn(0.0625f),
                 k72 = __float2half2_rn(-72.f);
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
-    const uint32_t h01 = g < 2 ? __byte_perm(vw[0].x, vw[1].x, sel) : __byte_perm(vw[0].y, vw[1].y, sel);
-    const uint32_t h89 = g < 2 ? __byte_perm(vw[2].x, vw[3].x, sel) : __byte_perm(vw[2].y, vw[3].y, sel);
+  for (int h = 0; h < H; ++h) {
+    // ---- P' of each group, as B fragments [keys][head]
+    const float va[4] = {bf16lo(vs[h][0].x), bf16hi(vs[h][0].x), bf16lo(vs[h][0].y), bf16hi(vs[h][0].y)};
+    const float vb[4] = {bf16lo(vs[h][1].x), bf16hi(vs[h][1].x), bf16lo(vs[h][1].y), bf16hi(vs[h][1].y)};
+    uint32_t pb[NT][4][2];
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const uint32_t y0 = m ? h01 >> 8 : h01, y1 = m ? h89 >> 8 : h89;
-      uint32_t a[4] = {(y0 & 0x000F000Fu) | 0x64006400u, (y0 & 0x00F000F0u) | 0x64006400u,
-                       (y1 & 0x000F000Fu) | 0x64006400u, (y1 & 0x00F000F0u) | 0x64006400u};
+    for (int nt = 0; nt < NT; ++nt) {
+      float p[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        __half2 hv = *reinterpret_cast<const __half2*>(&a[i]);
-        hv = (i & 1) ? __hfma2(hv, k16th, k72) : __hadd2(hv, k1032);
-        a[i] = *reinterpret_cast<const uint32_t*>(&hv);
+        p[i] = fast_exp2(fmaf(s[h][nt][i], st.f[nt][i & 1], sub[nt][i & 1]));
+        st.l[nt][i & 1] += p[i];
+        p[i] *= st.r_inv;
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        mma_f16_16816(st.o[nt][2 * g + m], a[0], a[1], a[2], a[3], pb[nt][g][0], pb[nt][g][1]);
+      for (int g = 0; g < 4; ++g) {
+        pb[nt][g][0] = movmatrix_trans(pack_h2(p[0] * va[g], p[1] * va[g]));
+        pb[nt][g][1] = movmatrix_trans(pack_h2(p[2] * vb[g], p[3] * vb[g]));
+      }
+    }
+    // ---- O^T: per group two 16-dim tiles; nibble j of a half word = tile j / 2,
+    // row gid + 8 (j % 2).  f16 bits 0x6400 | u = 1024 + u, 0x6400 | u << 4 =
+    // 1024 + 16 u.  vw: V words of keys 2t, 2t + 1, 2t + 8, 2t + 9
+    uint2 vw[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      vw[u] = *reinterpret_cast<const uint2*>(
+          rec + (16 * h + 2 * t + (u & 1) + 8 * (u >> 1)) * Q4_REC + Q4_V + 8 * gid);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
+      const uint32_t h01 = g < 2 ? __byte_perm(vw[0].x, vw[1].x, sel) : __byte_perm(vw[0].y, vw[1].y, sel);
+      const uint32_t h89 = g < 2 ? __byte_perm(vw[2].x, vw[3].x, sel) : __byte_perm(vw[2].y, vw[3].y, sel);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const uint32_t y0 = m ? h01 >> 8 : h01, y1 = m ? h89 >> 8 : h89;
+        uint32_t a[4] = {(y0 & 0x000F000Fu) | 0x64006400u, (y0 & 0x00F000F0u) | 0x64006400u,
+                         (y1 & 0x000F000Fu) | 0x64006400u, (y1 & 0x00F000F0u) | 0x64006400u};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          __half2 hv = *reinterpret_cast<const __half2*>(&a[i]);
+          hv = (i & 1) ? __hfma2(hv, k16th, k72) : __hadd2(hv, k1032);
+          a[i] = *reinterpret_cast<const uint32_t*>(&hv);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_f16_16816(st.o[nt][2 * g + m], a[0], a[1], a[2], a[3], pb[nt][g][0], pb[nt][g][1]);
+      }
     }
   }
 }

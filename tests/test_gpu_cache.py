@@ -160,6 +160,29 @@ def test_write_and_read_fp8(hs2, orc, n, H, cap, listed):
     assert hs2.hs2_get_device_status() == hs2.OK
 
 
+def test_write_fp8_quotients(hs2, orc):
+    """Codes of 2^21 quotients over many magnitudes (signed zeros and tiny
+    elements among them), equal to the oracle's."""
+    import torch
+    n, H = 4096, 2
+    rng = np.random.default_rng(17)
+    Kb, Vb = (rng.integers(0, 1 << 16, (n, H, 128)).astype(np.uint16) for _ in range(2))
+    for b in (Kb, Vb):  # each row pair within 2^30 of its largest element, or without any limit
+        top = rng.integers(1, 0x7F00, (n, H, 1))
+        low = np.where(rng.random((n, H, 1)) < 0.8, np.maximum(top - (12 << 7), 0), 0)
+        mag = low + (rng.random((n, H, 128)) * (top - low + 1)).astype(np.int64)
+        b[:] = (mag | (rng.integers(0, 2, mag.shape) << 15)).astype(np.uint16)
+        b[:, :, 7], b[:, :, 9] = 0x8000, 0
+    shape = hs2.Shape.make(n, H, H)
+    Kc = torch.empty(1, n, H, 128, dtype=torch.uint8, device="cuda")
+    Vc, S = torch.empty_like(Kc), torch.empty(1, n, H, device="cuda")
+    hs2.hs2_cache_write_fp8(dev_bf16(Kb), dev_bf16(Vb), None, Kc, Vc, S, shape)
+    ok, ov, os_ = np.empty((n, H, 128), np.uint8), np.empty((n, H, 128), np.uint8), np.empty((n, H), np.float32)
+    orc.lib().orc_quantize_rows(orc._p(Kb), orc._p(Vb), n * H, 128, orc._p(ok), orc._p(ov), orc._p(os_))
+    assert np.array_equal(S[0].cpu().numpy(), os_)
+    assert np.array_equal(Kc[0].cpu().numpy(), ok) and np.array_equal(Vc[0].cpu().numpy(), ov)
+
+
 def test_write_fp8_equals_the_bridge(hs2):
     """Rows that hs2_bridge_kv writes, quantised as written: the cache of
     hs2_bridge_kv_fp8, bit for bit."""
