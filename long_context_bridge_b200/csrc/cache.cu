@@ -59,8 +59,8 @@ __device__ __forceinline__ int64_t record_of(int64_t s, const SlotDiv& d, int h,
 // largest |x| of a lane's eight bf16 values, as bf16 bits (a NaN ranks above
 // an infinity, both above every finite value)
 __device__ __forceinline__ uint32_t amax_bits(const uint4& v) {
-  const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                              __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+  const uint32_t m = max_u16x2(max_u16x2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                               max_u16x2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
   return max(m >> 16, m & 0xFFFFu);
 }
 

@@ -38,6 +38,13 @@ __device__ __forceinline__ void stg_stream(void* p, const uint4& v) {
   __stcs(reinterpret_cast<uint4*>(p), v);
 }
 
+// the larger of each 16-bit half
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 struct Q4Scale {
   float inv;      // 1 / scale, within 2^-22 of it
   uint32_t bits;  // the scale's bf16 bits
@@ -157,13 +164,15 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 template <int NT>
 struct Q4State {
   uint32_t qf[NT][4][2][2];  // [group][MMA][register]
-  float q8[NT][4][2];        // -8 * sum of the group's q * 2^-24, heads 2t / 2t+1
+  float q8[NT][4][4];        // -8 * sum of the group's q * 2^-24, heads 2t, 2t+1, twice
   float f[NT][2];            // logit (base 2) = f * scaled sum (f > 0)
   float ref[NT][2], l[NT][2];
   float top[NT][2];          // (ref + 14) / f: a scaled sum above it moves ref
   float o[NT][8][4];
   uint32_t r_bits;           // bf16 bits of r2
+  uint32_t r_top;            // the largest bf16 below 2 r2, twice
   float r_inv;               // 1 / r2
+  uint32_t magic;            // 0x64006400 (see q4_step)
 };
 
 __device__ __forceinline__ float q4_pow2_bits(uint32_t bits) { return __uint_as_float(bits << 16); }
@@ -221,9 +230,11 @@ __device__ __forceinline__ void q4_init(Q4State<NT>& st, const __nv_bfloat16* __
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
       s *= -8.f / 16777216.f;
+      // an accumulator's four starts, from two lanes that hold the same sum: four
+      // registers of their own, or every MMA would first copy two of them
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        st.q8[nt][g][i] = __shfl_sync(0xffffffffu, s, 4 * (2 * t + i));
+      for (int i = 0; i < 4; ++i)
+        st.q8[nt][g][i] = __shfl_sync(0xffffffffu, s, 4 * (2 * t + (i & 1)) + (i >> 1));
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -234,7 +245,11 @@ __device__ __forceinline__ void q4_init(Q4State<NT>& st, const __nv_bfloat16* __
 #pragma unroll
     for (int i = 0; i < 8; ++i) st.o[nt][i][0] = st.o[nt][i][1] = st.o[nt][i][2] = st.o[nt][i][3] = 0.f;
   }
+  // as a value the compiler cannot see: with two constants, (x & mask) | magic
+  // became two instructions instead of one (the integer pipe bounds the step)
+  st.magic = __shfl_sync(0xffffffffu, 0x64006400u, 0);
   st.r_bits = 0x0080u;
+  st.r_top = 0x00FF00FFu;
   st.r_inv = q4_inv_pow2(st.r_bits);
 }
 
@@ -278,6 +293,7 @@ __device__ __forceinline__ void q4_raise(Q4State<NT>& st, const float (&s)[H][NT
   if (r > st.r_bits) {
     const float al = q4_pow2_bits(st.r_bits) * q4_inv_pow2(r);
     st.r_bits = r;
+    st.r_top = (r | 0x7Fu) * 0x00010001u;
     st.r_inv = q4_inv_pow2(r);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -323,7 +339,7 @@ __device__ __forceinline__ void q4_step(Q4State<NT>& st, const uint8_t* rec, int
         float c[4];
         mma_f16_16816(c, w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u,
                       st.qf[nt][g][0][0], st.qf[nt][g][0][1], st.q8[nt][g][0], st.q8[nt][g][1],
-                      st.q8[nt][g][0], st.q8[nt][g][1]);
+                      st.q8[nt][g][2], st.q8[nt][g][3]);
         mma_f16_16816(c, v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u,
                       st.qf[nt][g][1][0], st.qf[nt][g][1][1]);
 #pragma unroll
@@ -354,10 +370,9 @@ __device__ __forceinline__ void q4_step(Q4State<NT>& st, const uint8_t* rec, int
 #pragma unroll
       for (int i = 0; i < 4; ++i) raise |= s[h][nt][i] > st.top[nt][i & 1];
     }
-    vmax = __vmaxu2(vmax, __vmaxu2(__vmaxu2(vs[h][0].x, vs[h][0].y), __vmaxu2(vs[h][1].x, vs[h][1].y)));
+    vmax = max_u16x2(vmax, max_u16x2(max_u16x2(vs[h][0].x, vs[h][0].y), max_u16x2(vs[h][1].x, vs[h][1].y)));
   }
-  const uint32_t top = (st.r_bits | 0x7Fu) * 0x00010001u;
-  raise |= __vmaxu2(vmax, top) != top;
+  raise |= max_u16x2(vmax, st.r_top) != st.r_top;
   if (__any_sync(0xffffffffu, raise)) q4_raise<NT, H>(st, s, vs);
   float sub[NT][2];  // no key yet: ref = -inf, every logit = -inf, p = 0
 #pragma unroll
@@ -403,8 +418,8 @@ __device__ __forceinline__ void q4_step(Q4State<NT>& st, const uint8_t* rec, int
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const uint32_t y0 = m ? h01 >> 8 : h01, y1 = m ? h89 >> 8 : h89;
-        uint32_t a[4] = {(y0 & 0x000F000Fu) | 0x64006400u, (y0 & 0x00F000F0u) | 0x64006400u,
-                         (y1 & 0x000F000Fu) | 0x64006400u, (y1 & 0x00F000F0u) | 0x64006400u};
+        uint32_t a[4] = {(y0 & 0x000F000Fu) | st.magic, (y0 & 0x00F000F0u) | st.magic,
+                         (y1 & 0x000F000Fu) | st.magic, (y1 & 0x00F000F0u) | st.magic};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           __half2 hv = *reinterpret_cast<const __half2*>(&a[i]);
