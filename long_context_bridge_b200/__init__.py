@@ -314,159 +314,190 @@ def hs2_decode_cp_finish(n_ranks, sparse_recs, o_sparse, shape: Shape, stream=No
 # ---------------------------------------------------------------------------
 # rows into and out of a decode cache; the 4-bit cache
 # ---------------------------------------------------------------------------
-def _rows(t, n_heads, what):
-    """K or V rows [n, n_kv_heads, 128] bf16, dense but for the token stride."""
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+# These calls run once per decode step and layer, so their marshalling is kept
+# short: pointers as plain ints, one pass of checks per tensor, and the device
+# is only switched when the tensors do not live on the current one.
+def _on(t, dtype, what, dev):
+    """Checked device pointer of a dense tensor on device index `dev`."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dtype != BF16:
-        raise ValueError(f"{what} must be {BF16}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != n_heads or t.shape[2] != 128:
-        raise ValueError(f"{what} must be [n, {n_heads}, 128], got {tuple(t.shape)}")
-    st = t.stride()
-    if t.numel() and (st[2] != 1 or (n_heads > 1 and st[1] != 128)):
-        raise ValueError(f"the heads of {what} must be dense (strides [ld, 128, 1])")
-    ld = st[0] if t.shape[0] > 1 else n_heads * 128
-    return C.c_void_p(t.data_ptr()), ld
+    if t.dtype is not dtype:
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on cuda:{t.get_device()}, the cache on cuda:{dev}")
+    return t.data_ptr()
 
 
 def _shaped(t, shape, what):
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{what} must be {shape}, got {tuple(t.shape)}")
 
 
-def _one_device(*ts):
-    """The tensors' device; the call runs with it current and, unless a stream
-    is given, on that device's current stream."""
-    dev = ts[0].device
-    for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-    return torch.cuda.device(dev)
+def _run(fn, what, dev, stream, args):
+    """fn(*args, stream) with device `dev` current, on `stream` or, where that
+    is None, on that device's current stream."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)  # .current_stream(dev).cuda_stream
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status != OK:
+        raise HS2Error(status, what)
 
 
-def _row_args(K, V, slot, shape):
-    k, ldk = _rows(K, shape.n_kv_heads, "K")
-    v, ldv = _rows(V, shape.n_kv_heads, "V")
+def _rows(t, n_heads, what, dev):
+    """Pointer and token stride of K or V rows [n, n_kv_heads, 128] bf16, dense
+    but for that stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dtype is not BF16:
+        raise ValueError(f"{what} must be {BF16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != n_heads or t.shape[2] != 128:
+        raise ValueError(f"{what} must be [n, {n_heads}, 128], got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on cuda:{t.get_device()}, the cache on cuda:{dev}")
+    n = t.shape[0]
+    ld, head, dim = t.stride()
+    if n and (dim != 1 or (n_heads > 1 and head != 128)):
+        raise ValueError(f"the heads of {what} must be dense (strides [ld, 128, 1])")
+    return t.data_ptr(), ld if n > 1 else n_heads * 128
+
+
+def _row_args(K, V, slot, shape, dev):
+    k, ldk = _rows(K, shape.n_kv_heads, "K", dev)
+    v, ldv = _rows(V, shape.n_kv_heads, "V", dev)
     n = K.shape[0]
-    if V.shape[0] != n or (slot is not None and tuple(slot.shape) != (n,)):
+    if V.shape[0] != n or (slot is not None and slot.shape != (n,)):
         raise ValueError("K, V and slot must hold the same number of tokens")
-    return k, v, ldk, ldv, _ptr(slot, I32T, "slot", True), n
+    return k, v, ldk, ldv, None if slot is None else _on(slot, I32T, "slot", dev), n
 
 
 def _q4_cache(cache, shape):
-    """Pointer and batch of a 4-bit cache [batch, n_kv_heads, T, 144] uint8."""
-    p = _ptr(cache, U8, "cache")
-    if cache.dim() != 4 or tuple(cache.shape[1:]) != (shape.n_kv_heads, shape.T, Q4_RECORD_BYTES):
+    """Device index, pointer and batch of a 4-bit cache [batch, n_kv_heads, T, 144]."""
+    if not isinstance(cache, torch.Tensor) or not cache.is_cuda:
+        raise ValueError("cache must be a CUDA tensor")
+    dev = cache.get_device()
+    p = _on(cache, U8, "cache", dev)
+    if cache.dim() != 4 or cache.shape[1:] != (shape.n_kv_heads, shape.T, Q4_RECORD_BYTES):
         raise ValueError(f"cache must be [batch, {shape.n_kv_heads}, {shape.T}, {Q4_RECORD_BYTES}],"
                          f" got {tuple(cache.shape)}")
-    return p, cache.shape[0]
+    return dev, p, cache.shape[0]
 
 
 def _fp8_cache(Kc, Vc, scales, shape):
-    batch = Kc.shape[0]
-    _shaped(Kc, (batch, shape.T, shape.n_kv_heads, 128), "Kc")
-    _shaped(Vc, (batch, shape.T, shape.n_kv_heads, 128), "Vc")
+    """Device index, batch and pointers of an e4m3 cache and its scales."""
+    if not isinstance(Kc, torch.Tensor) or not Kc.is_cuda:
+        raise ValueError("Kc must be a CUDA tensor")
+    dev, batch = Kc.get_device(), Kc.shape[0]
+    ptrs = [_on(Kc, U8, "Kc", dev), _on(Vc, U8, "Vc", dev)]
+    rows = (batch, shape.T, shape.n_kv_heads)
+    _shaped(Kc, (*rows, 128), "Kc")
+    _shaped(Vc, (*rows, 128), "Vc")
     for s in scales:
-        _shaped(s, (batch, shape.T, shape.n_kv_heads), "scale")
-    return batch
+        ptrs.append(_on(s, F32, "scale", dev))
+        _shaped(s, rows, "scale")
+    return dev, batch, ptrs
 
 
 def hs2_cache_write_q4(K, V, slot, cache, shape: Shape, first=0, stream=None):
     """Quantises rows K, V [n, n_kv_heads, 128] (any token stride) into the
     4-bit cache [batch, n_kv_heads, T, 144] at slot [n] int32, or (slot None)
     at first, first + 1, ...; see include/hs2.h."""
-    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape)
-    c, batch = _q4_cache(cache, shape)
-    with _one_device(cache, K, V, slot):
-        _check(_lib.hs2_cache_write_q4(k, v, ldk, ldv, sl, int(first), n, c, batch, C.byref(shape),
-                                       _stream(stream)), "hs2_cache_write_q4")
+    dev, c, batch = _q4_cache(cache, shape)
+    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape, dev)
+    _run(_lib.hs2_cache_write_q4, "hs2_cache_write_q4", dev, stream,
+         (k, v, ldk, ldv, sl, first, n, c, batch, C.byref(shape)))
 
 
 def hs2_cache_read_q4(cache, slot, K, V, shape: Shape, first=0, stream=None):
-    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape)
-    c, batch = _q4_cache(cache, shape)
-    with _one_device(cache, K, V, slot):
-        _check(_lib.hs2_cache_read_q4(c, sl, int(first), n, k, v, ldk, ldv, batch, C.byref(shape),
-                                      _stream(stream)), "hs2_cache_read_q4")
+    """Cache rows (slots as in hs2_cache_write_q4) as bf16 into K, V; a row
+    whose slot is -1 stays as it was."""
+    dev, c, batch = _q4_cache(cache, shape)
+    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape, dev)
+    _run(_lib.hs2_cache_read_q4, "hs2_cache_read_q4", dev, stream,
+         (c, sl, first, n, k, v, ldk, ldv, batch, C.byref(shape)))
 
 
 def hs2_cache_write_fp8(K, V, slot, Kc, Vc, scale, shape: Shape, first=0, stream=None):
     """The e4m3 form of hs2_cache_write_q4: codes Kc, Vc [batch, T, n_kv_heads,
     128] and one fp32 scale per (token, KV head), the cache of hs2_block_decode."""
-    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape)
-    pk, pv, ps = _ptr(Kc, U8, "Kc"), _ptr(Vc, U8, "Vc"), _ptr(scale, F32, "scale")
-    batch = _fp8_cache(Kc, Vc, (scale,), shape)
-    with _one_device(Kc, Vc, scale, K, V, slot):
-        _check(_lib.hs2_cache_write_fp8(k, v, ldk, ldv, sl, int(first), n, pk, pv, ps, batch,
-                                        C.byref(shape), _stream(stream)), "hs2_cache_write_fp8")
+    dev, batch, ptrs = _fp8_cache(Kc, Vc, (scale,), shape)
+    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape, dev)
+    _run(_lib.hs2_cache_write_fp8, "hs2_cache_write_fp8", dev, stream,
+         (k, v, ldk, ldv, sl, first, n, *ptrs, batch, C.byref(shape)))
 
 
 def hs2_cache_read_fp8(Kc, Vc, k_scale, v_scale, slot, K, V, shape: Shape, first=0, stream=None):
-    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape)
-    pk, pv = _ptr(Kc, U8, "Kc"), _ptr(Vc, U8, "Vc")
-    pks, pvs = _ptr(k_scale, F32, "k_scale"), _ptr(v_scale, F32, "v_scale")
-    batch = _fp8_cache(Kc, Vc, (k_scale, v_scale), shape)
-    with _one_device(Kc, Vc, k_scale, v_scale, K, V, slot):
-        _check(_lib.hs2_cache_read_fp8(pk, pv, pks, pvs, sl, int(first), n, k, v, ldk, ldv, batch,
-                                       C.byref(shape), _stream(stream)), "hs2_cache_read_fp8")
+    """The e4m3 form of hs2_cache_read_q4."""
+    dev, batch, ptrs = _fp8_cache(Kc, Vc, (k_scale, v_scale), shape)
+    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape, dev)
+    _run(_lib.hs2_cache_read_fp8, "hs2_cache_read_fp8", dev, stream,
+         (*ptrs, sl, first, n, k, v, ldk, ldv, batch, C.byref(shape)))
+
+
+def _workspace(ws, dev):
+    return (None, 0) if ws is None else (_on(ws, U8, "workspace", dev), ws.numel())
 
 
 def hs2_decode_attn_q4(seq_len, q, cache, o, lse, shape: Shape, workspace, stream=None):
     """Attention of one new token per sequence over the 4-bit cache, with its
     lse; seq_len is a device int32 [batch] tensor read when the call runs."""
-    c, batch = _q4_cache(cache, shape)
+    dev, c, batch = _q4_cache(cache, shape)
     heads = (batch, shape.n_q_heads, 128)
-    pl, pq, po, ps = (_ptr(seq_len, I32T, "seq_len"), _ptr(q, BF16, "q"), _ptr(o, BF16, "o"),
-                      _ptr(lse, F32, "lse"))
     _shaped(seq_len, (batch,), "seq_len")
     _shaped(q, heads, "q")
     _shaped(o, heads, "o")
     _shaped(lse, heads[:2], "lse")
-    nbytes = 0 if workspace is None else workspace.numel()
-    with _one_device(cache, seq_len, q, o, lse, workspace):
-        _check(_lib.hs2_decode_attn_q4(batch, pl, pq, c, po, ps, C.byref(shape),
-                                       _ptr(workspace, U8, "workspace", True), nbytes,
-                                       _stream(stream)), "hs2_decode_attn_q4")
+    _run(_lib.hs2_decode_attn_q4, "hs2_decode_attn_q4", dev, stream,
+         (batch, _on(seq_len, I32T, "seq_len", dev), _on(q, BF16, "q", dev), c,
+          _on(o, BF16, "o", dev), _on(lse, F32, "lse", dev), C.byref(shape),
+          *_workspace(workspace, dev)))
 
 
 def hs2_sparse_attn_q4(q, cache, idx, o, lse, shape: Shape, stream=None):
     """Attention of one new token per sequence over the positions in idx
     [batch, n_kv_heads, k_global + window] of the 4-bit cache; lse may be None."""
-    c, batch = _q4_cache(cache, shape)
+    dev, c, batch = _q4_cache(cache, shape)
     heads = (batch, shape.n_q_heads, 128)
-    pq, pi, po, ps = (_ptr(q, BF16, "q"), _ptr(idx, I32T, "idx"), _ptr(o, BF16, "o"),
-                      _ptr(lse, F32, "lse", True))
     _shaped(q, heads, "q")
     _shaped(o, heads, "o")
     _shaped(idx, (batch, shape.n_kv_heads, shape.k_global + shape.window), "idx")
     if lse is not None:
         _shaped(lse, heads[:2], "lse")
-    with _one_device(cache, q, idx, o, lse):
-        _check(_lib.hs2_sparse_attn_q4(batch, pq, c, pi, po, ps, C.byref(shape), _stream(stream)),
-               "hs2_sparse_attn_q4")
+        lse = _on(lse, F32, "lse", dev)
+    _run(_lib.hs2_sparse_attn_q4, "hs2_sparse_attn_q4", dev, stream,
+         (batch, _on(q, BF16, "q", dev), c, _on(idx, I32T, "idx", dev), _on(o, BF16, "o", dev), lse,
+          C.byref(shape)))
 
 
 def hs2_block_decode_q4(seq_len, q_full, cache, o_full, lse, idx, q_sparse, o_sparse, shape: Shape,
                         workspace, stream=None):
     """hs2_block_decode over the 4-bit cache; seq_len is a host sequence of ints."""
-    c, batch = _q4_cache(cache, shape)
-    if len(seq_len) != batch or len(q_sparse) != len(o_sparse):
+    dev, c, batch = _q4_cache(cache, shape)
+    layers = len(q_sparse)
+    if len(seq_len) != batch or len(o_sparse) != layers:
         raise ValueError("seq_len must hold one length per sequence, o_sparse one output per layer")
     heads = (batch, shape.n_q_heads, 128)
-    pq, po, ps, pi = (_ptr(q_full, BF16, "q_full"), _ptr(o_full, BF16, "o_full"),
-                      _ptr(lse, F32, "lse"), _ptr(idx, I32T, "idx"))
-    for t, what in ((q_full, "q_full"), (o_full, "o_full"), *((t, "q_sparse") for t in q_sparse),
-                    *((t, "o_sparse") for t in o_sparse)):
-        _shaped(t, heads, what)
+    qs, os_ = (C.c_void_p * max(1, layers))(), (C.c_void_p * max(1, layers))()
+    for l in range(layers):
+        _shaped(q_sparse[l], heads, "q_sparse")
+        _shaped(o_sparse[l], heads, "o_sparse")
+        qs[l], os_[l] = _on(q_sparse[l], BF16, "q_sparse", dev), _on(o_sparse[l], BF16, "o_sparse", dev)
+    _shaped(q_full, heads, "q_full")
+    _shaped(o_full, heads, "o_full")
     _shaped(lse, heads[:2], "lse")
     _shaped(idx, (batch, shape.n_kv_heads, shape.k_global + shape.window), "idx")
-    qs, _keep_q = _ptr_array(q_sparse, BF16, "q_sparse")
-    os_, _keep_o = _ptr_array(o_sparse, BF16, "o_sparse")
-    nbytes = 0 if workspace is None else workspace.numel()
-    with _one_device(cache, q_full, o_full, lse, idx, workspace, *q_sparse, *o_sparse):
-        _check(_lib.hs2_block_decode_q4(batch, _i64s(seq_len), pq, c, po, ps, pi, len(q_sparse), qs,
-                                        os_, C.byref(shape), _ptr(workspace, U8, "workspace", True),
-                                        nbytes, _stream(stream)), "hs2_block_decode_q4")
+    PP = C.POINTER(C.c_void_p)
+    _run(_lib.hs2_block_decode_q4, "hs2_block_decode_q4", dev, stream,
+         (batch, (C.c_int64 * batch)(*seq_len), _on(q_full, BF16, "q_full", dev), c,
+          _on(o_full, BF16, "o_full", dev), _on(lse, F32, "lse", dev), _on(idx, I32T, "idx", dev),
+          layers, C.cast(qs, PP), C.cast(os_, PP), C.byref(shape), *_workspace(workspace, dev)))
 
 
 def hs2_get_device_status(stream=None) -> int:

@@ -11,10 +11,11 @@
 // a (sequence, KV head) ends.  There the warps' states are joined and one
 // partial (m, l, o) is written; decode_attn_q4_merge joins the partials.
 //
-// sparse_q4: a cluster of CTAs per (sequence, KV head) splits the list; lanes
-// copy the listed records into shared memory one by one (holes and entries out
-// of range closed up first), and the cluster joins through distributed shared
-// memory.
+// sparse_q4: a cluster of CTAs per (sequence, KV head) splits the list; each
+// warp gathers sixteen records at a time into a ring of its own by 16-byte
+// asynchronous copies, and the cluster joins through distributed shared memory.
+// (One bulk copy per 144-byte record was limited by the rate at which an SM
+// starts bulk copies, about one per 20 cycles.)
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -226,9 +227,9 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
         }
       };
       if (n >= WT)
-        q4_step<NT, WT / 16, true, LOGITS>(st, rec, WT, put);
+        q4_step<NT, WT / 16, true, LOGITS>(st, rec, ~0u, put);
       else
-        q4_step<NT, WT / 16, false, LOGITS>(st, rec, n, put);
+        q4_step<NT, WT / 16, false, LOGITS>(st, rec, (1u << n) - 1, put);
       if (LOGITS) lg += TILE * G;
       s_out = s_out + 1 == STAGES ? 0 : s_out + 1;
       --in_flight;
@@ -366,6 +367,10 @@ __global__ void __launch_bounds__(MW * 32)
 constexpr int SST = 4;                       // stages of 16 records per warp
 constexpr int SSTAGE_BYTES = 16 * Q4_REC;    // 2304
 
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 template <int NT>
 constexpr int sparse_smem_bytes() {
   return NW * SST * SSTAGE_BYTES + int(sizeof(JoinBuf<NT>)) + 16;
@@ -377,8 +382,7 @@ __global__ void __launch_bounds__(NW * 32)
               const int32_t* __restrict__ idx, __nv_bfloat16* __restrict__ O,
               float* __restrict__ lse, int64_t pairs, int64_t cap, int kw, float scale_log2) {
   constexpr int NT = G > 8 ? G / 8 : 1;
-  __shared__ uint64_t full[NW][SST];
-  // this CTA's joined state, read by the cluster's first CTA
+  // this CTA's joined state, read by the cluster's other CTAs
   __shared__ float cM[NT * 8], cL[NT * 8];
   __shared__ __align__(16) float cO[NT * 8][128];
   extern __shared__ uint8_t dsmem_raw[];
@@ -388,62 +392,60 @@ __global__ void __launch_bounds__(NW * 32)
   uint8_t* ring = dsmem + warp * SST * SSTAGE_BYTES;
   const int64_t pair = blockIdx.x / CS;
   const int crank = int(blockIdx.x % CS);
-  if (lane == 0) {
-    for (int i = 0; i < SST; ++i) mbar_init(&full[warp][i], 1);
-    fence_barrier_init();
-  }
-  __syncwarp();
   // this warp's entries: sixteens part, part + parts, ... of the list
   const int parts = CS * NW, part = crank * NW + warp;
   const int32_t* list = idx + pair * kw;
   const uint8_t* rows = cache + pair * cap * Q4_REC;
-  const int n16 = (kw + 15) / 16;
-  int issued = 0, used = 0;
-  int counts = 0;  // valid records of the stages in flight, 8 bits each
-  bool ok = true;
-  int e16 = part;
-  auto entry = [&](int at16) {
-    const int e = at16 * 16 + lane;
-    return lane < 16 && at16 < n16 && e < kw ? __ldg(list + e) : -1;
+  auto entry = [&](int e16) {
+    const int e = e16 * 16 + lane;
+    return lane < 16 && e < kw ? __ldg(list + e) : -1;
   };
-  int j_next = entry(e16);
-  auto fill = [&]() {
-    while (ok && e16 < n16 && issued - used < SST) {
-      int j = j_next;
-      e16 += parts;
-      j_next = entry(e16);
-      if (j != -1 && unsigned(j) >= unsigned(cap)) {
-        set_dev_status(DEV_BAD_INDEX);
-        j = -1;
-      }
-      const unsigned bal = __ballot_sync(0xffffffffu, j >= 0);
-      const int n = __popc(bal);
-      if (n == 0) continue;
-      const int s = issued % SST;
-      if (lane == 0) mbar_arrive_expect_tx(&full[warp][s], n * Q4_REC);
-      __syncwarp();
-      if (j >= 0)
-        bulk_load(ring + s * SSTAGE_BYTES + __popc(bal & ((1u << lane) - 1u)) * Q4_REC,
-                  rows + int64_t(j) * Q4_REC, Q4_REC, &full[warp][s]);
-      counts = (counts & ~(0xFF << (8 * s))) | (n << (8 * s));
-      ++issued;
+  // copies the records of one sixteen into stage s (one copy group, which may
+  // be empty) and returns which of its entries are valid: 144 pieces of 16
+  // bytes, piece p = part p % 9 of record p / 9
+  auto fill = [&](int j, int s) -> uint32_t {
+    if (j != -1 && unsigned(j) >= unsigned(cap)) {
+      set_dev_status(DEV_BAD_INDEX);
+      j = -1;
     }
+    const uint32_t keep = __ballot_sync(0xffffffffu, j >= 0);
+    if (keep != 0) {
+#pragma unroll
+      for (int k = 0; k < 5; ++k) {
+        const int p = lane + 32 * k, r = (p * 57) >> 9;  // p / 9 for p < 160
+        const int jr = __shfl_sync(0xffffffffu, j, r);   // r >= 16 (k = 4): lanes 16 .. hold -1
+        if (jr >= 0)
+          cp_async16(ring + s * SSTAGE_BYTES + 16 * p, rows + int64_t(jr) * Q4_REC + 16 * (p - 9 * r));
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    return keep;
   };
-  fill();
+  // the records are copied SST steps ahead of their use, the list is read one
+  // step further ahead
+  const int n_mine = ((kw + 15) / 16 - part + parts - 1) / parts;  // this warp's sixteens (<= 0: none)
+  uint64_t keeps = 0;  // of the stages, 16 bits each
+  int j[SST];
+#pragma unroll
+  for (int s = 0; s < SST; ++s) j[s] = entry(part + s * parts);
+  int j_next = entry(part + SST * parts);
+#pragma unroll
+  for (int s = 0; s < SST; ++s) keeps |= uint64_t(fill(j[s], s)) << (16 * s);
   Q4State<NT> st;
   q4_init<NT>(st, q + pair * G * 128, G, scale_log2);
-  while (used < issued) {
-    const int s = used % SST;
-    ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[warp][s], (used / SST) & 1));
-    const int nv = (counts >> (8 * s)) & 0xFF;
-    const auto none = [](int, int, const float (&)[4]) {};
-    if (nv == 16)
-      q4_step<NT, 1, true, false>(st, ring + s * SSTAGE_BYTES, nv, none);
-    else
-      q4_step<NT, 1, false, false>(st, ring + s * SSTAGE_BYTES, nv, none);
-    ++used;
-    __syncwarp();
-    fill();
+  const auto none = [](int, int, const float (&)[4]) {};
+  for (int i = 0; i < n_mine; ++i) {
+    const int s = i % SST;
+    const uint32_t keep = uint32_t(keeps >> (16 * s)) & 0xFFFFu;
+    asm volatile("cp.async.wait_group %0;" ::"n"(SST - 1) : "memory");
+    __syncwarp();  // every lane's pieces have landed
+    if (keep == 0xFFFFu)
+      q4_step<NT, 1, true, false>(st, ring + s * SSTAGE_BYTES, keep, none);
+    else if (keep != 0)
+      q4_step<NT, 1, false, false>(st, ring + s * SSTAGE_BYTES, keep, none);
+    __syncwarp();  // every lane has read the stage
+    keeps = (keeps & ~(uint64_t(0xFFFF) << (16 * s))) | uint64_t(fill(j_next, s)) << (16 * s);
+    j_next = entry(part + (i + SST + 1) * parts);
   }
   q4_put<NT>(st, join.m[warp], join.l[warp], join.o[warp]);
   __syncthreads();
@@ -501,9 +503,6 @@ __global__ void __launch_bounds__(NW * 32)
     if (lse != nullptr && lane == 0) lse[head] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
   }
   if constexpr (CS > 1) cluster.sync();  // shared memory stays until it has been read
-  if (lane == 0)
-    for (int s = 0; s < SST; ++s)
-      drain_phase(&full[warp][s], issued > s ? (issued - 1 - s) / SST + 1 : 0);
 }
 
 template <int G, bool LOGITS>

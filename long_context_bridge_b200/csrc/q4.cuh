@@ -304,12 +304,13 @@ __device__ __forceinline__ void q4_raise(Q4State<NT>& st, const float (&s)[H][NT
   }
 }
 
-// Attends the first nv (1 .. 16 H) of the 16 H records at `rec` (shared
-// memory); FULL: nv = 16 H.  on_logits(h, nt, x): the lane's base-2 logits of
-// keys 16 h + gid (heads 2t, 2t + 1) and 16 h + gid + 8 (the same heads), -inf
-// from key nv on.
+// Attends those of the 16 H records at `rec` (shared memory) whose bit of
+// `keep` is set; FULL: all of them (one instance without masks).  What a masked
+// record holds does not matter.  on_logits(h, nt, x): the lane's base-2 logits
+// of keys 16 h + gid (heads 2t, 2t + 1) and 16 h + gid + 8 (the same heads).
 template <int NT, int H, bool FULL, bool LOGITS, class F>
-__device__ __forceinline__ void q4_step(Q4State<NT>& st, const uint8_t* rec, int nv, F&& on_logits) {
+__device__ __forceinline__ void q4_step(Q4State<NT>& st, const uint8_t* rec, uint32_t keep,
+                                        F&& on_logits) {
   const int lane = lane_id(), gid = lane >> 2, t = lane & 3;
   float s[H][NT][4];
   uint2 vs[H][2];  // V scales of keys gid, gid + 8
@@ -325,8 +326,8 @@ __device__ __forceinline__ void q4_step(Q4State<NT>& st, const uint8_t* rec, int
     vs[h][0] = make_uint2(sa.z, sa.w);
     vs[h][1] = make_uint2(sb.z, sb.w);
     if (!FULL) {
-      if (16 * h + gid >= nv) vs[h][0] = make_uint2(0, 0);
-      if (16 * h + gid + 8 >= nv) vs[h][1] = make_uint2(0, 0);
+      if (!(keep >> (16 * h + gid) & 1)) vs[h][0] = make_uint2(0, 0);
+      if (!(keep >> (16 * h + gid + 8) & 1)) vs[h][1] = make_uint2(0, 0);
     }
     const uint32_t kw0[4] = {ka.x, ka.y, ka.z, ka.w}, kw1[4] = {kb.x, kb.y, kb.z, kb.w};
     const float ks0[4] = {bf16lo(sa.x), bf16hi(sa.x), bf16lo(sa.y), bf16hi(sa.y)};
@@ -360,7 +361,7 @@ __device__ __forceinline__ void q4_step(Q4State<NT>& st, const uint8_t* rec, int
       if (!FULL) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (16 * h + gid + 8 * (i >> 1) >= nv) s[h][nt][i] = -INFINITY;
+          if (!(keep >> (16 * h + gid + 8 * (i >> 1)) & 1)) s[h][nt][i] = -INFINITY;
       }
       if (LOGITS) {
         const float x[4] = {s[h][nt][0] * st.f[nt][0], s[h][nt][1] * st.f[nt][1],
