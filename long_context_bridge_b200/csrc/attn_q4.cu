@@ -38,15 +38,35 @@ constexpr int TILE = NW * WT;               // tokens per tile
 constexpr int STAGES = 3;                   // ring depth per warp
 constexpr int STAGE_BYTES = WT * Q4_REC;    // 4608
 
-template <int NT>
-struct JoinBuf {  // the four warps' states of one (sequence, KV head)
-  float m[NW][NT * 8], l[NW][NT * 8];
-  float o[NW][NT * 8][128];
+template <int NT, int W = NW>
+struct JoinBuf {  // the warps' states of one (sequence, KV head)
+  float m[W][NT * 8], l[W][NT * 8];
+  float o[W][NT * 8][128];
 };
 
 template <int NT>
 constexpr int attn_smem_bytes() {
   return NW * STAGES * STAGE_BYTES + int(sizeof(JoinBuf<NT>)) + 16;
+}
+
+// The joined state of W warps for head h: {m, l}, four dims per lane in acc.
+template <int NT, int W>
+__device__ __forceinline__ float2 joined(const JoinBuf<NT, W>& join, int h, int lane, float4& acc) {
+  float M = -INFINITY, L = 0.f;
+#pragma unroll
+  for (int i = 0; i < W; ++i) M = fmaxf(M, join.m[i][h]);
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const float w = join.m[i][h] == -INFINITY ? 0.f : fast_exp2(join.m[i][h] - M);
+    L += join.l[i][h] * w;
+    const float4 v = *reinterpret_cast<const float4*>(&join.o[i][h][4 * lane]);
+    acc.x += v.x * w;
+    acc.y += v.y * w;
+    acc.z += v.z * w;
+    acc.w += v.w * w;
+  }
+  return make_float2(M, L);
 }
 
 // length of sequence b, clamped to [0, cap]
@@ -243,25 +263,10 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
     __syncthreads();
     const int64_t slot = int64_t(blockIdx.x) + int64_t(b) * Hkv + g;
     for (int h = warp; h < G; h += NW) {
-      float M = -INFINITY, L = 0.f, w[NW];
-#pragma unroll
-      for (int i = 0; i < NW; ++i) M = fmaxf(M, join.m[i][h]);
-#pragma unroll
-      for (int i = 0; i < NW; ++i) {
-        w[i] = join.m[i][h] == -INFINITY ? 0.f : fast_exp2(join.m[i][h] - M);
-        L += join.l[i][h] * w[i];
-      }
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < NW; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(&join.o[i][h][4 * lane]);
-        acc.x += v.x * w[i];
-        acc.y += v.y * w[i];
-        acc.z += v.z * w[i];
-        acc.w += v.w * w[i];
-      }
+      float4 acc;
+      const float2 ml = joined<NT, NW>(join, h, lane, acc);
       *reinterpret_cast<float4*>(part_o + (slot * G + h) * 128 + 4 * lane) = acc;
-      if (lane == 0) part[slot * G + h] = make_float2(M, L);
+      if (lane == 0) part[slot * G + h] = ml;
     }
     __syncthreads();
   }
@@ -364,45 +369,48 @@ __global__ void __launch_bounds__(MW * 32)
 // ---------------------------------------------------------------------------
 // sparse_q4
 // ---------------------------------------------------------------------------
-constexpr int SST = 4;                       // stages of 16 records per warp
-constexpr int SSTAGE_BYTES = 16 * Q4_REC;    // 2304
+constexpr int SK = 32;                     // records per stage
+constexpr int SST = 2;                     // stages per warp
+constexpr int SSTAGE_BYTES = SK * Q4_REC;  // 4608
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-template <int NT>
+template <int NT, int W>
 constexpr int sparse_smem_bytes() {
-  return NW * SST * SSTAGE_BYTES + int(sizeof(JoinBuf<NT>)) + 16;
+  constexpr int ring = W * SST * SSTAGE_BYTES, join = int(sizeof(JoinBuf<NT, W>));
+  return (ring > join ? ring : join) + 16;  // the join reuses the drained ring
 }
 
 template <int G, int CS>
-__global__ void __launch_bounds__(NW * 32)
+__global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
     sparse_q4(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict__ cache,
               const int32_t* __restrict__ idx, __nv_bfloat16* __restrict__ O,
-              float* __restrict__ lse, int64_t pairs, int64_t cap, int kw, float scale_log2) {
-  constexpr int NT = G > 8 ? G / 8 : 1;
+              float* __restrict__ lse, int64_t cap, int kw, float scale_log2) {
+  constexpr int NT = G > 8 ? G / 8 : 1, W = NW;
   // this CTA's joined state, read by the cluster's other CTAs
-  __shared__ float cM[NT * 8], cL[NT * 8];
-  __shared__ __align__(16) float cO[NT * 8][128];
+  __shared__ float2 c_ml[NT * 8];
+  __shared__ __align__(16) float c_o[NT * 8][128];
   extern __shared__ uint8_t dsmem_raw[];
   uint8_t* dsmem = dsmem_raw + ((16u - (smem_u32(dsmem_raw) & 15u)) & 15u);
-  JoinBuf<NT>& join = *reinterpret_cast<JoinBuf<NT>*>(dsmem + NW * SST * SSTAGE_BYTES);
+  JoinBuf<NT, W>& join = *reinterpret_cast<JoinBuf<NT, W>*>(dsmem);
   const int warp = warp_id(), lane = lane_id();
   uint8_t* ring = dsmem + warp * SST * SSTAGE_BYTES;
   const int64_t pair = blockIdx.x / CS;
   const int crank = int(blockIdx.x % CS);
-  // this warp's entries: sixteens part, part + parts, ... of the list
-  const int parts = CS * NW, part = crank * NW + warp;
+  // this warp's entries [lo, hi) of the list, SK per step
+  const int per = (kw + CS * W - 1) / (CS * W);
+  const int lo = min(kw, (crank * W + warp) * per), hi = min(kw, lo + per);
   const int32_t* list = idx + pair * kw;
   const uint8_t* rows = cache + pair * cap * Q4_REC;
-  auto entry = [&](int e16) {
-    const int e = e16 * 16 + lane;
-    return lane < 16 && e < kw ? __ldg(list + e) : -1;
+  auto entry = [&](int step) {
+    const int e = lo + step * SK + lane;
+    return e < hi ? __ldg(list + e) : -1;
   };
-  // copies the records of one sixteen into stage s (one copy group, which may
-  // be empty) and returns which of its entries are valid: 144 pieces of 16
-  // bytes, piece p = part p % 9 of record p / 9
+  // copies the records of one step's entries into stage s (one copy group,
+  // which may be empty) and returns which of them are valid: SK * 9 pieces of
+  // 16 bytes, piece p = part p % 9 of record p / 9
   auto fill = [&](int j, int s) -> uint32_t {
     if (j != -1 && unsigned(j) >= unsigned(cap)) {
       set_dev_status(DEV_BAD_INDEX);
@@ -411,9 +419,9 @@ __global__ void __launch_bounds__(NW * 32)
     const uint32_t keep = __ballot_sync(0xffffffffu, j >= 0);
     if (keep != 0) {
 #pragma unroll
-      for (int k = 0; k < 5; ++k) {
-        const int p = lane + 32 * k, r = (p * 57) >> 9;  // p / 9 for p < 160
-        const int jr = __shfl_sync(0xffffffffu, j, r);   // r >= 16 (k = 4): lanes 16 .. hold -1
+      for (int k = 0; k < 9; ++k) {
+        const int p = lane + 32 * k, r = (p * 911) >> 13;  // p / 9 for p < 288
+        const int jr = __shfl_sync(0xffffffffu, j, r);
         if (jr >= 0)
           cp_async16(ring + s * SSTAGE_BYTES + 16 * p, rows + int64_t(jr) * Q4_REC + 16 * (p - 9 * r));
       }
@@ -421,88 +429,87 @@ __global__ void __launch_bounds__(NW * 32)
     asm volatile("cp.async.commit_group;" ::: "memory");
     return keep;
   };
-  // the records are copied SST steps ahead of their use, the list is read one
-  // step further ahead
-  const int n_mine = ((kw + 15) / 16 - part + parts - 1) / parts;  // this warp's sixteens (<= 0: none)
-  uint64_t keeps = 0;  // of the stages, 16 bits each
+  // records are copied SST steps ahead of their use, the list is read two
+  // steps further ahead
+  const int steps = (hi - lo + SK - 1) / SK;
   int j[SST];
 #pragma unroll
-  for (int s = 0; s < SST; ++s) j[s] = entry(part + s * parts);
-  int j_next = entry(part + SST * parts);
+  for (int s = 0; s < SST; ++s) j[s] = entry(s);
+  int j1 = entry(SST), j2 = entry(SST + 1);
+  uint32_t keep[SST];
 #pragma unroll
-  for (int s = 0; s < SST; ++s) keeps |= uint64_t(fill(j[s], s)) << (16 * s);
+  for (int s = 0; s < SST; ++s) keep[s] = fill(j[s], s);
   Q4State<NT> st;
   q4_init<NT>(st, q + pair * G * 128, G, scale_log2);
   const auto none = [](int, int, const float (&)[4]) {};
-  for (int i = 0; i < n_mine; ++i) {
-    const int s = i % SST;
-    const uint32_t keep = uint32_t(keeps >> (16 * s)) & 0xFFFFu;
+  int s = 0;
+  for (int i = 0; i < steps; ++i) {
     asm volatile("cp.async.wait_group %0;" ::"n"(SST - 1) : "memory");
     __syncwarp();  // every lane's pieces have landed
-    if (keep == 0xFFFFu)
-      q4_step<NT, 1, true, false>(st, ring + s * SSTAGE_BYTES, keep, none);
-    else if (keep != 0)
-      q4_step<NT, 1, false, false>(st, ring + s * SSTAGE_BYTES, keep, none);
+    const uint32_t k0 = keep[0];
+    if (k0 == 0xFFFFFFFFu)
+      q4_step<NT, SK / 16, true, false>(st, ring + s * SSTAGE_BYTES, k0, none);
+    else if (k0 != 0)
+      q4_step<NT, SK / 16, false, false>(st, ring + s * SSTAGE_BYTES, k0, none);
     __syncwarp();  // every lane has read the stage
-    keeps = (keeps & ~(uint64_t(0xFFFF) << (16 * s))) | uint64_t(fill(j_next, s)) << (16 * s);
-    j_next = entry(part + (i + SST + 1) * parts);
+#pragma unroll
+    for (int u = 0; u + 1 < SST; ++u) keep[u] = keep[u + 1];
+    keep[SST - 1] = fill(j1, s);
+    j1 = j2;
+    j2 = entry(i + SST + 2);
+    s = s + 1 == SST ? 0 : s + 1;
   }
+  __syncthreads();  // every warp is done with its ring (copies past the list's end are empty groups)
   q4_put<NT>(st, join.m[warp], join.l[warp], join.o[warp]);
   __syncthreads();
-  namespace cg = cooperative_groups;
-  for (int h = warp; h < G; h += NW) {
-    float M = -INFINITY, L = 0.f, w[NW];
-#pragma unroll
-    for (int i = 0; i < NW; ++i) M = fmaxf(M, join.m[i][h]);
-#pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      w[i] = join.m[i][h] == -INFINITY ? 0.f : fast_exp2(join.m[i][h] - M);
-      L += join.l[i][h] * w[i];
-    }
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      const float4 v = *reinterpret_cast<const float4*>(&join.o[i][h][4 * lane]);
-      acc.x += v.x * w[i];
-      acc.y += v.y * w[i];
-      acc.z += v.z * w[i];
-      acc.w += v.w * w[i];
-    }
-    *reinterpret_cast<float4*>(&cO[h][4 * lane]) = acc;
-    if (lane == 0) {
-      cM[h] = M;
-      cL[h] = L;
-    }
-  }
-  cg::cluster_group cluster = cg::this_cluster();
-  if constexpr (CS > 1) cluster.sync(); else __syncwarp();
-  // heads are spread over the cluster's CTAs
-  for (int h = crank + CS * warp; h < G; h += CS * NW) {
-    float m[CS], M = -INFINITY, L = 0.f;
-#pragma unroll
-    for (int c = 0; c < CS; ++c) {
-      m[c] = CS > 1 ? *cluster.map_shared_rank(&cM[h], c) : cM[h];
-      M = fmaxf(M, m[c]);
-    }
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int c = 0; c < CS; ++c) {
-      const float w = m[c] == -INFINITY ? 0.f : fast_exp2(m[c] - M);
-      L += (CS > 1 ? *cluster.map_shared_rank(&cL[h], c) : cL[h]) * w;
-      const float* src = CS > 1 ? cluster.map_shared_rank(&cO[h][0], c) : &cO[h][0];
-      const float4 v = *reinterpret_cast<const float4*>(src + 4 * lane);
-      acc.x += v.x * w;
-      acc.y += v.y * w;
-      acc.z += v.z * w;
-      acc.w += v.w * w;
-    }
-    const float inv = L == 0.f ? 0.f : 1.f / L;  // an empty list: o = 0, lse = -inf
+  auto store = [&](int h, float2 ml, const float4& acc) {
+    const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;  // an empty list: o = 0, lse = -inf
     const int64_t head = pair * G + h;
     *reinterpret_cast<uint2*>(O + head * 128 + 4 * lane) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (lse != nullptr && lane == 0) lse[head] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
+    if (lse != nullptr && lane == 0)
+      lse[head] = ml.y == 0.f ? -INFINITY : (ml.x + __log2f(ml.y)) * kLn2;
+  };
+  for (int h = warp; h < G; h += W) {
+    float4 acc;
+    const float2 ml = joined<NT, W>(join, h, lane, acc);
+    if (CS == 1) {
+      store(h, ml, acc);
+    } else {
+      *reinterpret_cast<float4*>(&c_o[h][4 * lane]) = acc;
+      if (lane == 0) c_ml[h] = ml;
+    }
   }
-  if constexpr (CS > 1) cluster.sync();  // shared memory stays until it has been read
+  if constexpr (CS > 1) {
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    // heads are spread over the cluster's CTAs
+    for (int h = crank + CS * warp; h < G; h += CS * W) {
+      float2 ml[CS];
+      float4 v[CS];
+#pragma unroll
+      for (int c = 0; c < CS; ++c) {
+        ml[c] = *cluster.map_shared_rank(&c_ml[h], c);
+        v[c] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(&c_o[h][0], c) + 4 * lane);
+      }
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int c = 0; c < CS; ++c) M = fmaxf(M, ml[c].x);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < CS; ++c) {
+        const float w = ml[c].x == -INFINITY ? 0.f : fast_exp2(ml[c].x - M);
+        L += ml[c].y * w;
+        acc.x += v[c].x * w;
+        acc.y += v[c].y * w;
+        acc.z += v[c].z * w;
+        acc.w += v[c].w * w;
+      }
+      store(h, make_float2(M, L), acc);
+    }
+    cluster.sync();  // shared memory stays until it has been read
+  }
 }
 
 template <int G, bool LOGITS>
@@ -542,15 +549,14 @@ cudaError_t launch_attn_g(const Q4AttnArgs& a, cudaStream_t st) {
 
 template <int G, int CS>
 cudaError_t launch_sparse_cs(const Q4SparseArgs& a, cudaStream_t st) {
-  constexpr int NT = G > 8 ? G / 8 : 1;
+  constexpr int NT = G > 8 ? G / 8 : 1, W = NW;
   const auto kernel = sparse_q4<G, CS>;
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), sparse_smem_bytes<NT>());
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), sparse_smem_bytes<NT, W>());
   if (e != cudaSuccess) return e;
-  const int64_t pairs = int64_t(a.B) * a.Hkv;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(pairs * CS));
-  cfg.blockDim = dim3(NW * 32);
-  cfg.dynamicSmemBytes = sparse_smem_bytes<NT>();
+  cfg.gridDim = dim3(unsigned(int64_t(a.B) * a.Hkv * CS));
+  cfg.blockDim = dim3(W * 32);
+  cfg.dynamicSmemBytes = sparse_smem_bytes<NT, W>();
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -558,13 +564,29 @@ cudaError_t launch_sparse_cs(const Q4SparseArgs& a, cudaStream_t st) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = CS > 1 ? 1 : 0;
   e = cudaLaunchKernelEx(&cfg, kernel, reinterpret_cast<const __nv_bfloat16*>(a.q),
-                         a.cache, a.idx, reinterpret_cast<__nv_bfloat16*>(a.o), a.lse, pairs,
-                         a.cap, a.kw, a.scale * kLog2e);
+                         a.cache, a.idx, reinterpret_cast<__nv_bfloat16*>(a.o), a.lse, a.cap, a.kw,
+                         a.scale * kLog2e);
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
+}
+
+// How many CTAs share a list.  More of them shorten the chain of steps of a
+// warp, until the launch no longer fits the GPU at once (its second wave costs
+// as much as the first) or a warp's part falls below one step of 32 entries.
+// Measured, us: lists of 1152, G = 8: 32 lists 13.9 / 10.8 / 8.8 / 9.1 for 1 /
+// 2 / 4 / 8 CTAs, 64 lists 14.4 / 11.3 / 10.6 / 17.9, 256 lists 20.0 / 25.2 /
+// 32.5 / 50.8; one list of 2304, G = 16: 29.3 / 18.0 / 12.9 / 11.2; lists of
+// 128: 4.2 / 5.7 / 5.7 / 6.7.
+template <int G>
+cudaError_t launch_sparse_g(const Q4SparseArgs& a, cudaStream_t st) {
+  const int64_t pairs = int64_t(a.B) * a.Hkv;
+  if (pairs * 8 <= 148 && a.kw >= 8 * NW * SK) return launch_sparse_cs<G, 8>(a, st);
+  if (pairs * 4 <= 2 * 148 && a.kw >= 4 * NW * SK) return launch_sparse_cs<G, 4>(a, st);
+  if (pairs * 2 <= 2 * 148 && a.kw >= 2 * NW * SK) return launch_sparse_cs<G, 2>(a, st);
+  return launch_sparse_cs<G, 1>(a, st);
 }
 
 }  // namespace
@@ -591,11 +613,11 @@ cudaError_t launch_attn_q4(const Q4AttnArgs& a, cudaStream_t st) {
 
 cudaError_t launch_sparse_q4(const Q4SparseArgs& a, cudaStream_t st) {
   switch (a.Hq / a.Hkv) {
-    case 1: return launch_sparse_cs<1, 8>(a, st);
-    case 2: return launch_sparse_cs<2, 8>(a, st);
-    case 4: return launch_sparse_cs<4, 8>(a, st);
-    case 8: return launch_sparse_cs<8, 8>(a, st);
-    case 16: return launch_sparse_cs<16, 8>(a, st);
+    case 1: return launch_sparse_g<1>(a, st);
+    case 2: return launch_sparse_g<2>(a, st);
+    case 4: return launch_sparse_g<4>(a, st);
+    case 8: return launch_sparse_g<8>(a, st);
+    case 16: return launch_sparse_g<16>(a, st);
     default: return cudaErrorInvalidValue;
   }
 }
