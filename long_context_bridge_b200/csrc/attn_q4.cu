@@ -35,7 +35,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int NW = 4;                       // warps per CTA
 constexpr int WT = 32;                      // tokens per warp and tile
 constexpr int TILE = NW * WT;               // tokens per tile
-constexpr int STAGES = 3;                   // ring depth per warp
+constexpr int STAGES = 2;                   // ring depth per warp (a power of two)
 constexpr int STAGE_BYTES = WT * Q4_REC;    // 4608
 
 template <int NT, int W = NW>
@@ -181,83 +181,94 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
   if (blockIdx.x >= n_ranges) return;
   const int64_t t0 = total * blockIdx.x / n_ranges, t1 = total * (blockIdx.x + 1) / n_ranges;
 
-  // ---- this warp's copies: its part of each tile of the range, in order
-  TileAt ahead = tile_at(t0, s_pre, lens, B, cap, Hkv);
-  TileAt at = ahead;
-  int64_t left = t1 - t0;   // tiles still to copy
-  int run = 0;              // of them, tiles of the (sequence, KV head) being copied
-  int rest = 0;             // its tokens from this warp's part of the next tile on
-  const uint8_t* src = nullptr;
-  int s_in = 0, s_out = 0;  // stage filled next / attended next
-  int in_flight = 0;
-  unsigned ph = 0, odd = 0, filled = 0;  // per stage: phase to wait for; fills odd; any
-  bool ok = true;
-  auto fill = [&]() {  // copies tiles until the ring is full
-    while (left > 0 && in_flight < STAGES) {
-      if (run == 0) {
-        run = int(min(left, int64_t(ahead.nt - ahead.i)));
-        rest = ahead.len - ahead.i * TILE - warp * WT;
-        src = cache + ((int64_t(ahead.b) * Hkv + ahead.g) * cap + int64_t(ahead.i) * TILE + warp * WT) * Q4_REC;
-      }
-      if (rest > 0) {
-        if (lane == 0) {
-          const uint32_t bytes = min(rest, WT) * Q4_REC;
-          mbar_arrive_expect_tx(&full[warp][s_in], bytes);
-          bulk_load(ring + s_in * STAGE_BYTES, src, bytes, &full[warp][s_in]);
-        }
-        filled |= 1u << s_in;
-        odd ^= 1u << s_in;
-        s_in = s_in + 1 == STAGES ? 0 : s_in + 1;
-        ++in_flight;
-      }
-      rest -= TILE;
-      src += TILE * Q4_REC;
-      --left;
-      if (--run == 0) {
-        ahead.i = ahead.nt - 1;
-        tile_next(ahead, s_pre, lens, B, cap, Hkv);
-      }
-    }
+  // ---- this warp's records of a range: per (sequence, KV head) some whole
+  // parts of WT records and at most one shorter one, copied in order
+  struct Run {
+    int whole, part;     // whole parts; records of the short one (0: none)
+    const uint8_t* src;  // the first
   };
-  fill();
+  auto run_of = [&](const TileAt& a, int64_t tiles) {
+    const int n = a.len - a.i * TILE - warp * WT;  // tokens from this warp's first part on
+    Run r;
+    r.whole = min(int(tiles), n >= WT ? (n - WT) / TILE + 1 : 0);
+    r.part = r.whole < tiles ? max(0, min(WT - 1, n - r.whole * TILE)) : 0;
+    r.src = cache + ((int64_t(a.b) * Hkv + a.g) * cap + int64_t(a.i) * TILE + warp * WT) * Q4_REC;
+    return r;
+  };
+  auto next_head = [&](TileAt& a) {
+    a.i = a.nt - 1;
+    tile_next(a, s_pre, lens, B, cap, Hkv);
+  };
+  TileAt at = tile_at(t0, s_pre, lens, B, cap, Hkv), ahead = at;
+  int64_t left = t1 - t0;  // tiles whose copies have not been reached
+  Run run{0, 0, nullptr};
+  unsigned n_in = 0, n_out = 0;  // stages filled / attended so far
+  bool ok = true;
+  auto fill = [&]() {  // copies the next part
+    while (run.whole == 0 && run.part == 0) {
+      if (left == 0) return;
+      const int64_t tiles = min(left, int64_t(ahead.nt - ahead.i));
+      run = run_of(ahead, tiles);
+      left -= tiles;
+      next_head(ahead);
+    }
+    const uint32_t bytes = (run.whole > 0 ? WT : run.part) * Q4_REC;
+    if (run.whole > 0) --run.whole; else run.part = 0;
+    if (lane == 0) {
+      uint64_t* bar = &full[warp][n_in % STAGES];
+      mbar_arrive_expect_tx(bar, bytes);
+      bulk_load(ring + (n_in % STAGES) * STAGE_BYTES, run.src, bytes, bar);
+    }
+    run.src += TILE * Q4_REC;
+    ++n_in;
+  };
+#pragma unroll 1
+  for (int s = 0; s < STAGES; ++s) fill();
 
   for (int64_t tt = t0; tt < t1;) {
     // ---- one (sequence, KV head): its tiles in this CTA's range
     const int b = at.b, g = at.g;
-    const int tiles = int(min(t1 - tt, int64_t(at.nt - at.i)));
+    const int64_t tiles = min(t1 - tt, int64_t(at.nt - at.i));
+    const Run mine = run_of(at, tiles);
     tt += tiles;
     Q4State<NT> st;
     q4_init<NT>(st, q + (int64_t(b) * Hkv + g) * G * 128, G, scale_log2);
-    int n = at.len - at.i * TILE - warp * WT;  // tokens from this warp's part on
     float* lg = LOGITS ? logits + ((int64_t(b) * Hkv + g) * cap + at.i * TILE + warp * WT + gid) * G + 2 * t
                        : nullptr;
-    for (int i = 0; i < tiles && n > 0; ++i, n -= TILE) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[warp][s_out], (ph >> s_out) & 1));
-      ph ^= 1u << s_out;
-      const uint8_t* rec = ring + s_out * STAGE_BYTES;
-      auto put = [&](int h, int nt, const float (&x)[4]) {
-        const int h0 = nt * 8 + 2 * t, nv = n - 16 * h;
-        float* r = lg + 16 * h * G + nt * 8;
-        if (h0 + 1 < G) {
-          if (gid < nv) *reinterpret_cast<float2*>(r) = make_float2(x[0], x[1]);
-          if (gid + 8 < nv) *reinterpret_cast<float2*>(r + 8 * G) = make_float2(x[2], x[3]);
-        } else if (h0 < G) {
-          if (gid < nv) r[0] = x[0];
-          if (gid + 8 < nv) r[8 * G] = x[2];
-        }
-      };
-      if (n >= WT)
-        q4_step<NT, WT / 16, true, LOGITS>(st, rec, ~0u, put);
-      else
-        q4_step<NT, WT / 16, false, LOGITS>(st, rec, (1u << n) - 1, put);
-      if (LOGITS) lg += TILE * G;
-      s_out = s_out + 1 == STAGES ? 0 : s_out + 1;
-      --in_flight;
+    int n = WT;  // records of the part being attended
+    auto put = [&](int h, int nt, const float (&x)[4]) {
+      const int h0 = nt * 8 + 2 * t, nv = n - 16 * h;
+      float* r = lg + 16 * h * G + nt * 8;
+      if (h0 + 1 < G) {
+        if (gid < nv) *reinterpret_cast<float2*>(r) = make_float2(x[0], x[1]);
+        if (gid + 8 < nv) *reinterpret_cast<float2*>(r + 8 * G) = make_float2(x[2], x[3]);
+      } else if (h0 < G) {
+        if (gid < nv) r[0] = x[0];
+        if (gid + 8 < nv) r[8 * G] = x[2];
+      }
+    };
+    auto arrive = [&]() {  // the next stage's records, once they have landed
+      if (!__all_sync(0xffffffffu, mbar_try_wait(&full[warp][n_out % STAGES], (n_out / STAGES) & 1)) && ok)
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[warp][n_out % STAGES], (n_out / STAGES) & 1));
+      return ring + (n_out % STAGES) * STAGE_BYTES;
+    };
+    auto release = [&]() {
+      ++n_out;
       __syncwarp();  // every lane has read the stage before it is filled again
       if (ok) fill();
+    };
+#pragma unroll 1
+    for (int i = 0; i < mine.whole; ++i) {
+      q4_step<NT, WT / 16, true, LOGITS>(st, arrive(), ~0u, put);
+      if (LOGITS) lg += TILE * G;
+      release();
     }
-    at.i = at.nt - 1;
-    tile_next(at, s_pre, lens, B, cap, Hkv);
+    if (mine.part > 0) {
+      n = mine.part;
+      q4_step<NT, WT / 16, false, LOGITS>(st, arrive(), (1u << n) - 1, put);
+      release();
+    }
+    next_head(at);
     // ---- join the warps and write the partial
     q4_put<NT>(st, join.m[warp], join.l[warp], join.o[warp]);
     __syncthreads();
@@ -272,9 +283,8 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
   }
   // after a wait that ran out: every copy that was issued lands before exit
   if (!ok && lane == 0)
-    for (int s = 0; s < STAGES; ++s)
-      if ((filled >> s) & 1)
-        mbar_wait_budget(&full[warp][s], ((odd >> s) & 1) ^ 1, kDrainBudgetCycles);
+    for (unsigned s = 0; s < STAGES; ++s)
+      drain_phase(&full[warp][s], n_in > s ? (n_in - 1 - s) / STAGES + 1 : 0);
 }
 
 // grid (Hkv * G, B): the partials of (b, head) -> o, lse.  Each of MW warps
