@@ -21,20 +21,21 @@ HS2_STATUS_ACCESSOR(status_cache)
 
 namespace {
 
-constexpr int TOK = 4;       // tokens per warp
+constexpr int TOK = 4;       // tokens per warp, a power of two (8: 134 us where 4 takes 129)
 constexpr int CW_WARPS = 4;  // warps per CTA
 
-// s / cap for s < 2^31: mul = floor(2^shift / cap) + 1 with shift = 31 +
-// ceil(log2 cap) is 2^shift / cap (1 + e), 0 < e <= 2^-31, so s * mul / 2^shift
-// exceeds s / cap by less than 1 / cap and has the same whole part.
+// s / cap for s < 2^31, cap > 1: mul = floor(2^(31 + l) / cap) + 1 with l =
+// ceil(log2 cap) is 2^(31 + l) / cap (1 + e), 0 < e <= 2^-31, so s * mul /
+// 2^(31 + l) exceeds s / cap by less than 1 / cap and has the same whole part.
+// cap > 2^(l - 1) keeps mul below 2^32.
 struct SlotDiv {
-  uint64_t mul;
-  uint32_t shift, cap;
+  uint32_t mul, shift, cap;  // shift = l - 1 behind a 32-bit multiply-high
 };
 SlotDiv slot_div(int64_t cap) {
-  uint32_t l = 0;
+  uint32_t l = 1;
   while ((int64_t(1) << l) < cap) ++l;
-  return SlotDiv{(uint64_t(1) << (31 + l)) / uint64_t(cap) + 1, 31 + l, uint32_t(cap)};
+  return SlotDiv{cap == 1 ? 0u : uint32_t((uint64_t(1) << (31 + l)) / uint64_t(cap) + 1), l - 1,
+                 uint32_t(cap)};
 }
 
 // The cache slot of token i, or -1 for none (a slot outside [0, n_slots) is
@@ -49,11 +50,11 @@ __device__ __forceinline__ int64_t token_slot(const int32_t* __restrict__ slot, 
   return -1;
 }
 
-// Record of slot s (s < 2^31): s / cap by the precomputed reciprocal.
+// Index of slot s's record (s >= 0; -1 stays -1).
 __device__ __forceinline__ int64_t record_of(int64_t s, const SlotDiv& d, int h, int Hkv) {
-  const uint32_t b = uint32_t((uint64_t(uint32_t(s)) * d.mul) >> d.shift);
-  const uint32_t p = uint32_t(s) - b * d.cap;
-  return (int64_t(b) * Hkv + h) * d.cap + p;
+  if (s < 0) return -1;
+  const uint32_t b = d.cap == 1 ? uint32_t(s) : __umulhi(uint32_t(s), d.mul) >> d.shift;
+  return (int64_t(b) * Hkv + h) * d.cap + (uint32_t(s) - b * d.cap);
 }
 
 // largest |x| of a lane's eight bf16 values, as bf16 bits (a NaN ranks above
@@ -97,12 +98,15 @@ __global__ void __launch_bounds__(CW_WARPS * 32)
   if (i0 >= n) return;
   const __nv_bfloat16* src = (is_v ? V : K) + h * 128 + m * 8;
   const int64_t ld = is_v ? ldv : ldk;
-  int64_t at[TOK];
+  // lane u % TOK finds where token u goes
+  const int64_t mine = record_of(token_slot(slot, first, i0 + lane % TOK, n, n_slots), div, h, Hkv);
+  const uint32_t live = __ballot_sync(0xffffffffu, mine >= 0);
   uint4 v[TOK];
+  src += i0 * ld;
 #pragma unroll
   for (int u = 0; u < TOK; ++u) {
-    at[u] = token_slot(slot, first, i0 + u, n, n_slots);
-    v[u] = at[u] >= 0 ? ldg_stream(src + (i0 + u) * ld) : make_uint4(0, 0, 0, 0);
+    v[u] = live >> u & 1 ? ldg_stream(src) : make_uint4(0, 0, 0, 0);
+    src += ld;
   }
 #pragma unroll
   for (int u = 0; u < TOK; ++u) {
@@ -117,8 +121,8 @@ __global__ void __launch_bounds__(CW_WARPS * 32)
     if (is_v) w = wv;
     // the pair of groups (g, g ^ 1): the even one stores both scales
     const uint32_t s2 = __shfl_xor_sync(0xffffffffu, sc.bits, 4);
-    if (at[u] < 0) continue;
-    uint8_t* rec = cache + record_of(at[u], div, h, Hkv) * Q4_REC;
+    uint8_t* rec = cache + __shfl_sync(0xffffffffu, mine, u) * Q4_REC;
+    if (!(live >> u & 1)) continue;
     reinterpret_cast<uint32_t*>(rec + (is_v ? Q4_V : Q4_K))[stored_word(is_v, g, t)] = w;
     if (t == 0 && (g & 1) == 0)
       reinterpret_cast<uint32_t*>(rec + (is_v ? Q4_VS : Q4_KS))[g >> 1] = sc.bits | (s2 << 16);
@@ -135,16 +139,16 @@ __global__ void __launch_bounds__(CW_WARPS * 32)
   const int m = lane & 15, g = m >> 2, t = m & 3;
   const int64_t i0 = (int64_t(blockIdx.x) * CW_WARPS + warp_id()) * TOK;
   if (i0 >= n) return;
-  __nv_bfloat16* dst = (is_v ? V : K) + h * 128 + m * 8;
   const int64_t ld = is_v ? ldv : ldk;
-  int64_t at[TOK];
+  __nv_bfloat16* dst = (is_v ? V : K) + h * 128 + m * 8 + i0 * ld;
+  const int64_t mine = record_of(token_slot(slot, first, i0 + lane % TOK, n, n_slots), div, h, Hkv);
+  const uint32_t live = __ballot_sync(0xffffffffu, mine >= 0);
   uint32_t w[TOK], s[TOK];
 #pragma unroll
   for (int u = 0; u < TOK; ++u) {
-    at[u] = token_slot(slot, first, i0 + u, n, n_slots);
+    const uint8_t* rec = cache + __shfl_sync(0xffffffffu, mine, u) * Q4_REC;
     w[u] = s[u] = 0;
-    if (at[u] >= 0) {
-      const uint8_t* rec = cache + record_of(at[u], div, h, Hkv) * Q4_REC;
+    if (live >> u & 1) {
       w[u] = __ldg(reinterpret_cast<const uint32_t*>(rec + (is_v ? Q4_V : Q4_K)) +
                    stored_word(is_v, g, t));
       s[u] = __ldg(reinterpret_cast<const uint16_t*>(rec + (is_v ? Q4_VS : Q4_KS)) + g);
@@ -153,9 +157,8 @@ __global__ void __launch_bounds__(CW_WARPS * 32)
 #pragma unroll
   for (int u = 0; u < TOK; ++u) {
     const uint32_t wv = v_trade(w[u], g);  // its own inverse
-    const uint32_t x = is_v ? wv : w[u];
-    if (at[u] < 0) continue;
-    stg_stream(dst + (i0 + u) * ld, q4_values8(x, s[u]));
+    if (live >> u & 1) stg_stream(dst, q4_values8(is_v ? wv : w[u], s[u]));
+    dst += ld;
   }
 }
 
@@ -191,18 +194,21 @@ __global__ void __launch_bounds__(CW_WARPS * 32)
   if (i0 >= n) return;
   const __nv_bfloat16* src = (is_v ? V : K) + h * 128 + m * 8;
   const int64_t ld = is_v ? ldv : ldk;
-  int64_t at[TOK];
+  const int mine = int(token_slot(slot, first, i0 + lane % TOK, n, n_slots));
+  const uint32_t live = __ballot_sync(0xffffffffu, mine >= 0);
   uint4 v[TOK];
+  src += i0 * ld;
 #pragma unroll
   for (int u = 0; u < TOK; ++u) {
-    at[u] = token_slot(slot, first, i0 + u, n, n_slots);
-    v[u] = at[u] >= 0 ? ldg_stream(src + (i0 + u) * ld) : make_uint4(0, 0, 0, 0);
+    v[u] = live >> u & 1 ? ldg_stream(src) : make_uint4(0, 0, 0, 0);
+    src += ld;
   }
 #pragma unroll
   for (int u = 0; u < TOK; ++u) {
     // one scale for the row pair: the largest |x| over K and V
     const uint32_t a = __reduce_max_sync(0xffffffffu, amax_bits(v[u]));
-    if (at[u] < 0) continue;
+    const int64_t row = int64_t(__shfl_sync(0xffffffffu, mine, u)) * Hkv + h;
+    if (!(live >> u & 1)) continue;
     const bool finite = a < 0x7F80u;
     const float amax = __uint_as_float(a << 16);
     const float s = a == 0 ? 1.f : finite ? amax / 448.f : __uint_as_float(0x7FC00000u);
@@ -219,7 +225,6 @@ __global__ void __launch_bounds__(CW_WARPS * 32)
       for (int i = 0; i < 4; ++i)
         c[i >> 1] |= e4m3x2(x[2 * i] / s, x[2 * i + 1] / s) << (16 * (i & 1));
     }
-    const int64_t row = at[u] * Hkv + h;
     *reinterpret_cast<uint2*>((is_v ? Vc : Kc) + row * 128 + m * 8) = make_uint2(c[0], c[1]);
     if (lane == 0) scale[row] = s;
   }
@@ -245,25 +250,24 @@ __global__ void __launch_bounds__(CW_WARPS * 32)
   const int m = lane & 15;
   const int64_t i0 = (int64_t(blockIdx.x) * CW_WARPS + warp_id()) * TOK;
   if (i0 >= n) return;
-  __nv_bfloat16* dst = (is_v ? V : K) + h * 128 + m * 8;
   const int64_t ld = is_v ? ldv : ldk;
-  int64_t at[TOK];
+  __nv_bfloat16* dst = (is_v ? V : K) + h * 128 + m * 8 + i0 * ld;
+  const int mine = int(token_slot(slot, first, i0 + lane % TOK, n, n_slots));
+  const uint32_t live = __ballot_sync(0xffffffffu, mine >= 0);
   uint2 c[TOK];
   float s[TOK];
 #pragma unroll
   for (int u = 0; u < TOK; ++u) {
-    at[u] = token_slot(slot, first, i0 + u, n, n_slots);
+    const int64_t row = int64_t(__shfl_sync(0xffffffffu, mine, u)) * Hkv + h;
     c[u] = make_uint2(0, 0);
     s[u] = 0.f;
-    if (at[u] >= 0) {
-      const int64_t row = at[u] * Hkv + h;
+    if (live >> u & 1) {
       c[u] = __ldg(reinterpret_cast<const uint2*>((is_v ? Vc : Kc) + row * 128 + m * 8));
       s[u] = __ldg((is_v ? vs : ks) + row);
     }
   }
 #pragma unroll
   for (int u = 0; u < TOK; ++u) {
-    if (at[u] < 0) continue;
     const uint32_t w[2] = {c[u].x, c[u].y};
     uint32_t o[4];
 #pragma unroll
@@ -271,7 +275,8 @@ __global__ void __launch_bounds__(CW_WARPS * 32)
       const float2 f = e4m3x2_f32(w[i >> 1] >> (16 * (i & 1)));
       o[i] = pack_bf16x2(f.x * s[u], f.y * s[u]);
     }
-    stg_stream(dst + (i0 + u) * ld, make_uint4(o[0], o[1], o[2], o[3]));
+    if (live >> u & 1) stg_stream(dst, make_uint4(o[0], o[1], o[2], o[3]));
+    dst += ld;
   }
 }
 
