@@ -393,11 +393,17 @@ constexpr int sparse_smem_bytes() {
   return (ring > join ? ring : join) + 16;  // the join reuses the drained ring
 }
 
+struct Q4Layers {
+  const void* q[kQ4MaxLayers];
+  void* o[kQ4MaxLayers];
+};
+
+// grid (CS * pairs, layers)
 template <int G, int CS>
 __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
-    sparse_q4(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict__ cache,
-              const int32_t* __restrict__ idx, __nv_bfloat16* __restrict__ O,
-              float* __restrict__ lse, int64_t cap, int kw, float scale_log2) {
+    sparse_q4(const __grid_constant__ Q4Layers layers, const uint8_t* __restrict__ cache,
+              const int32_t* __restrict__ idx, float* __restrict__ lse, int64_t cap, int kw,
+              float scale_log2) {
   constexpr int NT = G > 8 ? G / 8 : 1, W = NW;
   // this CTA's joined state, read by the cluster's other CTAs
   __shared__ float2 c_ml[NT * 8];
@@ -409,6 +415,8 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
   uint8_t* ring = dsmem + warp * SST * SSTAGE_BYTES;
   const int64_t pair = blockIdx.x / CS;
   const int crank = int(blockIdx.x % CS);
+  const auto* q = reinterpret_cast<const __nv_bfloat16*>(layers.q[blockIdx.y]);
+  auto* O = reinterpret_cast<__nv_bfloat16*>(layers.o[blockIdx.y]);
   // this warp's entries [lo, hi) of the list, SK per step
   const int per = (kw + CS * W - 1) / (CS * W);
   const int lo = min(kw, (crank * W + warp) * per), hi = min(kw, lo + per);
@@ -564,7 +572,12 @@ cudaError_t launch_sparse_cs(const Q4SparseArgs& a, cudaStream_t st) {
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), sparse_smem_bytes<NT, W>());
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(int64_t(a.B) * a.Hkv * CS));
+  Q4Layers layers{};
+  for (int l = 0; l < a.layers; ++l) {
+    layers.q[l] = a.q[l];
+    layers.o[l] = a.o[l];
+  }
+  cfg.gridDim = dim3(unsigned(int64_t(a.B) * a.Hkv * CS), unsigned(a.layers));
   cfg.blockDim = dim3(W * 32);
   cfg.dynamicSmemBytes = sparse_smem_bytes<NT, W>();
   cfg.stream = st;
@@ -575,9 +588,7 @@ cudaError_t launch_sparse_cs(const Q4SparseArgs& a, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CS > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kernel, reinterpret_cast<const __nv_bfloat16*>(a.q),
-                         a.cache, a.idx, reinterpret_cast<__nv_bfloat16*>(a.o), a.lse, a.cap, a.kw,
-                         a.scale * kLog2e);
+  e = cudaLaunchKernelEx(&cfg, kernel, layers, a.cache, a.idx, a.lse, a.cap, a.kw, a.scale * kLog2e);
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
@@ -592,7 +603,7 @@ cudaError_t launch_sparse_cs(const Q4SparseArgs& a, cudaStream_t st) {
 // 128: 4.2 / 5.7 / 5.7 / 6.7.
 template <int G>
 cudaError_t launch_sparse_g(const Q4SparseArgs& a, cudaStream_t st) {
-  const int64_t pairs = int64_t(a.B) * a.Hkv;
+  const int64_t pairs = int64_t(a.B) * a.Hkv * a.layers;  // lists x layers
   if (pairs * 8 <= 148 && a.kw >= 8 * NW * SK) return launch_sparse_cs<G, 8>(a, st);
   if (pairs * 4 <= 2 * 148 && a.kw >= 4 * NW * SK) return launch_sparse_cs<G, 4>(a, st);
   if (pairs * 2 <= 2 * 148 && a.kw >= 2 * NW * SK) return launch_sparse_cs<G, 2>(a, st);

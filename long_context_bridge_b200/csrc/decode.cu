@@ -40,6 +40,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -514,14 +516,14 @@ __global__ void __launch_bounds__(128)
 }
 
 // ---------------------------------------------------------------------------
-// decode_score: grid (chunks, Hkv, B), 256 threads
+// decode_score: grid (chunks of ch keys, Hkv, B), 256 threads
 // ---------------------------------------------------------------------------
 __device__ int block_kth_bucket(const uint32_t* __restrict__ gh, uint32_t k, uint32_t* s_scan);
 
 template <int G>
 __global__ void __launch_bounds__(256)
     decode_score(const float* __restrict__ logits, const float* __restrict__ lse2,
-                 SeqLens seq_len, int64_t cap, int Hkv, int k, int w,
+                 SeqLens seq_len, int64_t cap, int Hkv, int k, int w, int ch,
                  float* __restrict__ score, uint32_t* __restrict__ hist,
                  uint32_t* __restrict__ done, int* __restrict__ kth_bucket) {
   __shared__ uint32_t sh[NBUCKET];
@@ -536,8 +538,9 @@ __global__ void __launch_bounds__(256)
   const int64_t lo = seq_len.lo[b];  // logits and scores are indexed by j - lo
   const float* lg = logits + (size_t(b) * Hkv + g) * cap * G;
   float* sc = score + (size_t(b) * Hkv + g) * cap;
-  const int64_t j_hi = min(lo + int64_t(c + 1) * CH, j_end);
-  for (int64_t j = lo + int64_t(c) * CH + threadIdx.x; j < j_hi; j += 256) {
+  const int64_t j_hi = min(lo + int64_t(c + 1) * ch, j_end);
+#pragma unroll 4
+  for (int64_t j = lo + int64_t(c) * ch + threadIdx.x; j < j_hi; j += 256) {
     // the G logits of key j: 16-byte loads where G allows
     float x[G];
     if constexpr (G % 4 == 0) {
@@ -617,19 +620,19 @@ __device__ int block_kth_bucket(const uint32_t* __restrict__ gh, uint32_t k, uin
 }
 
 // ---------------------------------------------------------------------------
-// decode_collect: grid (chunks, Hkv, B), 256 threads
+// decode_collect: grid (chunks of ch keys, Hkv, B), 256 threads
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256)
     decode_collect(const float* __restrict__ score, const int* __restrict__ kth_bucket,
-                   SeqLens seq_len, int64_t cap, int Hkv, int k, int w,
+                   SeqLens seq_len, int64_t cap, int Hkv, int k, int w, int ch,
                    uint2* __restrict__ cand, uint32_t* __restrict__ ccount) {
   const int c = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int N = seq_len.n[b];
   const int64_t s_lo = seq_len.lo[b];
   const int64_t s_hi = min(int64_t(N) - w, int64_t(seq_len.hi[b]));  // slice candidates [s_lo, s_hi)
   if (s_hi - s_lo <= k) return;  // every candidate is selected; decode_final writes them
-  const int64_t j_lo = s_lo + int64_t(c) * CH;
-  const int64_t j_hi = min(j_lo + CH, s_hi);
+  const int64_t j_lo = s_lo + int64_t(c) * ch;
+  const int64_t j_hi = min(j_lo + ch, s_hi);
   if (j_lo >= j_hi) return;
   const size_t bg = size_t(b) * Hkv + g;
   const int kb = kth_bucket[bg];
@@ -695,6 +698,94 @@ __device__ void block_bitonic_u64(uint64_t* s, int np, bool descending) {
     }
 }
 
+// The k largest of the n > k > 0 distinct keys s[0 .. n): radix select from the
+// highest bit in which they differ, ten bits a pass.  On return the keys x with
+// (x >> shift) >= (prefix >> shift) are the k largest.  512 threads.
+struct KeyCut {
+  uint64_t prefix;
+  int shift;
+};
+__device__ KeyCut block_top_k(const uint64_t* s, int n, uint32_t k, uint32_t* s_hist) {
+  __shared__ uint64_t s_lo[16], s_hi[16];
+  __shared__ uint32_t s_sum[16], s_pick[3];
+  const int tid = threadIdx.x, lane = lane_id(), warp = warp_id();
+  uint64_t hi = 0, lo = ~uint64_t(0);
+  for (int e = tid; e < n; e += 512) {
+    hi = max(hi, s[e]);
+    lo = min(lo, s[e]);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+  }
+  if (lane == 0) {
+    s_hi[warp] = hi;
+    s_lo[warp] = lo;
+  }
+  __syncthreads();
+  for (int i = 0; i < 16; ++i) {
+    hi = max(hi, s_hi[i]);
+    lo = min(lo, s_lo[i]);
+  }
+  int top = 64 - __clzll(hi ^ lo);  // bits below this one are still open (n > 1: top >= 1)
+  KeyCut cut{top == 64 ? 0 : (hi >> top) << top, top};
+  while (true) {
+    const int w = min(10, top), shift = top - w;
+    const uint32_t mask = (1u << w) - 1;
+    s_hist[tid] = s_hist[tid + 512] = 0;
+    __syncthreads();
+    for (int e = tid; e < n; e += 512) {
+      const uint64_t x = s[e];
+      if (top == 64 || (x >> top) == (cut.prefix >> top)) atomicAdd(&s_hist[(x >> shift) & mask], 1u);
+    }
+    __syncthreads();
+    // bins from the top: thread t holds bins 1023 - 2 t and 1022 - 2 t
+    const uint32_t a = s_hist[1023 - 2 * tid], b = s_hist[1022 - 2 * tid];
+    uint32_t inc = a + b;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += v;
+    }
+    if (lane == 31) s_sum[warp] = inc;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) inc += s_sum[i];
+    const uint32_t before = inc - a - b;
+    if (before < k && k <= inc) {  // one thread
+      const bool first = before + a >= k;
+      s_pick[0] = 1023 - 2 * tid - (first ? 0 : 1);
+      s_pick[1] = k - before - (first ? 0 : a);
+      s_pick[2] = first ? a : b;
+    }
+    __syncthreads();
+    cut.prefix |= uint64_t(s_pick[0]) << shift;
+    cut.shift = top = shift;
+    k = s_pick[1];
+    if (s_pick[2] == k || top == 0) return cut;  // the whole bin belongs to the k largest
+  }
+}
+
+// Ascending sort of s[0 .. np), np a power of two, in place: a bitonic network
+// whose steps within a warp's 2 np / 16 words need no CTA barrier.  512 threads.
+__device__ void block_sort_u32(uint32_t* s, int np) {
+  const int lane = lane_id(), warp = warp_id();
+  const int seg = max(64, np / 16);  // words per warp
+  for (int size = 2; size <= np; size <<= 1)
+    for (int stride = size >> 1; stride > 0; stride >>= 1) {
+      if (stride >= seg / 2) __syncthreads(); else __syncwarp();
+      for (int i = warp * (seg / 2) + lane; i < min(np / 2, (warp + 1) * (seg / 2)); i += 32) {
+        const int lo = 2 * stride * (i / stride) + (i % stride), hi = lo + stride;
+        const uint32_t a = s[lo], b = s[hi];
+        if ((a > b) == ((lo & size) == 0)) {
+          s[lo] = b;
+          s[hi] = a;
+        }
+      }
+    }
+  __syncthreads();
+}
+
 // What decode_final reads and writes.
 //   FINAL_FULL   the whole block on one device: the top k of the candidate
 //                list (or, when it overflowed, of every candidate's score),
@@ -725,6 +816,7 @@ __global__ void __launch_bounds__(512)
   extern __shared__ uint64_t sk[];  // CAPC keys
   __shared__ uint32_t s_hist[256];
   __shared__ uint32_t s_misc[4];
+  __shared__ uint32_t s_wide[1024], s_pos[2048];  // k <= 2048
   const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   const int N = seq_len.n[b];
   const int64_t i = N - 1;
@@ -757,8 +849,9 @@ __global__ void __launch_bounds__(512)
   }
   const uint32_t n = MODE == FINAL_MERGE ? uint32_t(io.n_ranks) * uint32_t(k) : io.ccount[bg];
   if (n <= uint32_t(CAPC)) {
-    int np = 1;
-    while (np < int(n)) np <<= 1;
+    int np = int(n);  // a power of two where the keys are sorted
+    if (MODE == FINAL_LOCAL)
+      for (np = 1; np < int(n);) np <<= 1;
     for (int e = tid; e < np; e += blockDim.x) {
       if (e < int(n)) {
         const uint2 v = MODE == FINAL_MERGE
@@ -770,21 +863,34 @@ __global__ void __launch_bounds__(512)
       }
     }
     __syncthreads();
-    block_bitonic_u64(sk, np, true);  // best first
     if (MODE == FINAL_LOCAL) {
+      block_bitonic_u64(sk, np, true);  // best first
       for (int e = tid; e < k; e += blockDim.x)
         rec[e] = make_uint2(uint32_t(sk[e] >> 32), ~uint32_t(sk[e]));
       return;
     }
     // the k best positions, ascending
+    if (k == 0) return;
+    uint32_t* pos = s_pos;
     int kp = 1;
     while (kp < k) kp <<= 1;
+    KeyCut cut{0, 63};
+    if (n > uint32_t(k)) cut = block_top_k(sk, int(n), uint32_t(k), s_wide);
+    if (tid == 0) s_misc[3] = 0;
+    for (int e = k + tid; e < kp; e += blockDim.x) pos[e] = 0xFFFFFFFFu;
     __syncthreads();
-    for (int e = tid; e < kp; e += blockDim.x)
-      sk[e] = e < k ? uint64_t(~uint32_t(sk[e])) : ~uint64_t(0);
+    for (int e0 = 0; e0 < int(n); e0 += blockDim.x) {
+      const int e = e0 + tid;
+      const bool take = e < int(n) && (n <= uint32_t(k) || (sk[e] >> cut.shift) >= (cut.prefix >> cut.shift));
+      const uint32_t bal = __ballot_sync(0xffffffffu, take);
+      uint32_t at = 0;
+      if (lane_id() == 0 && bal) at = atomicAdd(&s_misc[3], uint32_t(__popc(bal)));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(bal & ((1u << lane_id()) - 1u));
+      if (take) pos[at] = ~uint32_t(sk[e]);
+    }
     __syncthreads();
-    block_bitonic_u64(sk, kp, false);
-    for (int e = tid; e < k; e += blockDim.x) out[e] = int32_t(sk[e]);
+    block_sort_u32(pos, kp);
+    for (int e = tid; e < k; e += blockDim.x) out[e] = int32_t(pos[e]);
     return;
   }
   // overflow (FULL / LOCAL): exact radix select over every candidate's score,
@@ -940,11 +1046,15 @@ cudaError_t launch_dec_g(const DecodeArgs& a, const SeqLens& d_seq, int max_len,
     e = cudaMemsetAsync(ccount, 0, size_t(B) * Hkv * 8, st);  // counts and tickets
     if (e != cudaSuccess) return e;
     if (nch_used > 0) {
-      decode_score<G><<<dim3(nch_used, Hkv, B), 256, 0, st>>>(logits, lse2, d_seq, a.cap, Hkv,
-                                                              a.k, a.w, score, hist, done,
-                                                              kth_bucket);
-      decode_collect<<<dim3(nch_used, Hkv, B), 256, 0, st>>>(score, kth_bucket, d_seq, a.cap,
-                                                             Hkv, a.k, a.w, cand, ccount);
+      // keys per scoring CTA: 8192, or fewer (down to 1024) where that leaves
+      // the GPU without four CTAs per SM
+      int ch = CH;
+      while (ch > 1024 && int64_t((max_len + ch - 1) / ch) * Hkv * B < 4 * 148) ch /= 2;
+      const dim3 grid((max_len + ch - 1) / ch, Hkv, B);
+      decode_score<G><<<grid, 256, 0, st>>>(logits, lse2, d_seq, a.cap, Hkv, a.k, a.w, ch, score,
+                                            hist, done, kth_bucket);
+      decode_collect<<<grid, 256, 0, st>>>(score, kth_bucket, d_seq, a.cap, Hkv, a.k, a.w, ch, cand,
+                                           ccount);
       launches += 2;
     }
     const int fsmem = CAPC * 8;
@@ -987,9 +1097,23 @@ cudaError_t launch_dec_g(const DecodeArgs& a, const SeqLens& d_seq, int max_len,
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (a.cache4 != nullptr) {
-    for (int l = 0; l < a.n_sparse; ++l) {
-      const Q4SparseArgs s{a.qs[l], a.cache4, a.idx,   a.os[l],  nullptr, B,
-                           a.cap,   Hq,       Hkv,     a.scale,  a.k + a.w};
+    // every layer's queries are there: the layers go together, a launch per
+    // kQ4MaxLayers of them
+    for (int l0 = 0; l0 < a.n_sparse; l0 += kQ4MaxLayers) {
+      Q4SparseArgs s{};
+      s.layers = std::min(kQ4MaxLayers, a.n_sparse - l0);
+      for (int l = 0; l < s.layers; ++l) {
+        s.q[l] = a.qs[l0 + l];
+        s.o[l] = a.os[l0 + l];
+      }
+      s.cache = a.cache4;
+      s.idx = a.idx;
+      s.B = B;
+      s.cap = a.cap;
+      s.Hq = Hq;
+      s.Hkv = Hkv;
+      s.scale = a.scale;
+      s.kw = a.k + a.w;
       e = launch_sparse_q4(s, st);
       if (e != cudaSuccess) return e;
     }

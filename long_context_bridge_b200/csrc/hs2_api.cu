@@ -670,8 +670,19 @@ hs2_status hs2_sparse_attn_q4(int32_t batch, const hs2_bf16* q, const hs2_q4* ca
   HS2_NEED(q && cache && idx && o);
   HS2_NEED(aligned16(q) && aligned16(cache) && aligned4(idx) && aligned16(o) && aligned4(lse));
   if (int64_t(batch) * s->n_kv_heads > INT32_MAX / 8) return HS2_ERR_UNSUPPORTED;
-  const Q4SparseArgs a{q,    cache,        idx,           o,        lse, batch,
-                       s->T, s->n_q_heads, s->n_kv_heads, s->scale, s->k_global + s->window};
+  Q4SparseArgs a{};
+  a.layers = 1;
+  a.q[0] = q;
+  a.o[0] = o;
+  a.cache = cache;
+  a.idx = idx;
+  a.lse = lse;
+  a.B = batch;
+  a.cap = s->T;
+  a.Hq = s->n_q_heads;
+  a.Hkv = s->n_kv_heads;
+  a.scale = s->scale;
+  a.kw = s->k_global + s->window;
   return cuda_status(launch_sparse_q4(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -264,12 +264,14 @@ struct Q4AttnArgs {
 size_t attn_q4_workspace_bytes(int B, int Hq, int Hkv);
 cudaError_t launch_attn_q4(const Q4AttnArgs& a, cudaStream_t stream);
 
+constexpr int kQ4MaxLayers = 8;
 struct Q4SparseArgs {
-  const void* q;  // bf16 [B][Hq][128]
+  int layers;                   // sharing cache and idx
+  const void* q[kQ4MaxLayers];  // bf16 [B][Hq][128] each
+  void* o[kQ4MaxLayers];
   const uint8_t* cache;
   const int32_t* idx;  // [B][Hkv][kw]
-  void* o;
-  float* lse;  // nullable
+  float* lse;  // nullable, of the only layer
   int B;
   int64_t cap;
   int Hq, Hkv;
