@@ -626,6 +626,11 @@ __global__ void __launch_bounds__(256)
     decode_collect(const float* __restrict__ score, const int* __restrict__ kth_bucket,
                    SeqLens seq_len, int64_t cap, int Hkv, int k, int w, int ch,
                    uint2* __restrict__ cand, uint32_t* __restrict__ ccount) {
+  // candidates gather here first, so that a CTA takes its place in the (b, g)
+  // list with one atomic
+  constexpr uint32_t LISTC = 1024;
+  __shared__ uint2 s_list[LISTC];
+  __shared__ uint32_t s_n, s_base;
   const int c = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int N = seq_len.n[b];
   const int64_t s_lo = seq_len.lo[b];
@@ -638,7 +643,8 @@ __global__ void __launch_bounds__(256)
   const int kb = kth_bucket[bg];
   const uint32_t thr = kb < 0 ? 0u : uint32_t(kb);
   const float* sc = score + bg * cap;  // score of key j at sc[j - s_lo]
-  const int lane = lane_id();
+  if (threadIdx.x == 0) s_n = 0;
+  __syncthreads();
   const bool vec = (cap & 3) == 0;  // rows of scores start 16-byte aligned
   // in local indices x = j - s_lo: rounds of 2048 keys from a multiple of 4
   // at or below x_lo; thread owns keys x0 .. x0+3 and x0+1024 .. x0+1027
@@ -664,19 +670,25 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int64_t xl = base + 1024 * (e >> 2) + 4 * threadIdx.x + (e & 3);
-      const int64_t j = xl + s_lo;
-      const bool take = xl >= x_lo && xl < x_hi && (__float_as_uint(v[e]) >> 20) >= thr;
-      const uint32_t bal = __ballot_sync(0xffffffffu, take);
-      if (bal) {
-        uint32_t pos = 0;
-        if (lane == __ffs(bal) - 1) pos = atomicAdd(&ccount[bg], __popc(bal));
-        pos = __shfl_sync(0xffffffffu, pos, __ffs(bal) - 1);
-        const uint32_t p = pos + __popc(bal & ((1u << lane) - 1u));
-        if (take && p < uint32_t(CAPC))
-          cand[bg * CAPC + p] = make_uint2(__float_as_uint(v[e]), uint32_t(j));
+      if (xl >= x_lo && xl < x_hi && (__float_as_uint(v[e]) >> 20) >= thr) {
+        const uint32_t p = atomicAdd(&s_n, 1u);
+        const uint2 r = make_uint2(__float_as_uint(v[e]), uint32_t(xl + s_lo));
+        if (p < LISTC) {
+          s_list[p] = r;
+        } else {  // more than the list holds: straight to global memory
+          const uint32_t q = atomicAdd(&ccount[bg], 1u);
+          if (q < uint32_t(CAPC)) cand[bg * CAPC + q] = r;
+        }
       }
     }
   }
+  __syncthreads();
+  const uint32_t m = min(s_n, LISTC);
+  if (m == 0) return;
+  if (threadIdx.x == 0) s_base = atomicAdd(&ccount[bg], m);
+  __syncthreads();
+  for (uint32_t e = threadIdx.x; e < m; e += 256)
+    if (s_base + e < uint32_t(CAPC)) cand[bg * CAPC + s_base + e] = s_list[e];
 }
 
 // ---------------------------------------------------------------------------
@@ -686,7 +698,7 @@ __device__ void block_bitonic_u64(uint64_t* s, int np, bool descending) {
   for (int size = 2; size <= np; size <<= 1)
     for (int stride = size >> 1; stride > 0; stride >>= 1) {
       for (int i = threadIdx.x; i < np / 2; i += blockDim.x) {
-        const int lo = 2 * stride * (i / stride) + (i % stride), hi = lo + stride;
+        const int lo = 2 * i - (i & (stride - 1)), hi = lo + stride;
         const bool up = ((lo & size) == 0) != descending;
         const uint64_t a = s[lo], bb = s[hi];
         if ((a > bb) == up) {
@@ -775,7 +787,7 @@ __device__ void block_sort_u32(uint32_t* s, int np) {
     for (int stride = size >> 1; stride > 0; stride >>= 1) {
       if (stride >= seg / 2) __syncthreads(); else __syncwarp();
       for (int i = warp * (seg / 2) + lane; i < min(np / 2, (warp + 1) * (seg / 2)); i += 32) {
-        const int lo = 2 * stride * (i / stride) + (i % stride), hi = lo + stride;
+        const int lo = 2 * i - (i & (stride - 1)), hi = lo + stride;
         const uint32_t a = s[lo], b = s[hi];
         if ((a > b) == ((lo & size) == 0)) {
           s[lo] = b;
@@ -1041,9 +1053,8 @@ cudaError_t launch_dec_g(const DecodeArgs& a, const SeqLens& d_seq, int max_len,
     ++launches;
   }
   if (full || a.step == DEC_CP_SELECT) {
-    e = cudaMemsetAsync(hist, 0, size_t(B) * Hkv * NBUCKET * 4, st);
-    if (e != cudaSuccess) return e;
-    e = cudaMemsetAsync(ccount, 0, size_t(B) * Hkv * 8, st);  // counts and tickets
+    // histograms, counts and tickets (adjacent: the histograms fill whole 256 bytes)
+    e = cudaMemsetAsync(hist, 0, size_t(B) * Hkv * (NBUCKET * 4 + 8), st);
     if (e != cudaSuccess) return e;
     if (nch_used > 0) {
       // keys per scoring CTA: 8192, or fewer (down to 1024) where that leaves
