@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
     decode_attn_q4(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict__ cache,
                    const __grid_constant__ Q4Lens lens, int B, int64_t cap, int Hkv,
                    float scale_log2, float* __restrict__ logits, float2* __restrict__ part,
-                   float* __restrict__ part_o) {
+                   float* __restrict__ part_o, int2* __restrict__ where) {
   constexpr int NT = G > 8 ? G / 8 : 1;
   __shared__ int s_pre[kQ4MaxBatch + 1];
   __shared__ int s_sum[NW];
@@ -230,6 +230,12 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
     const int b = at.b, g = at.g;
     const int64_t tiles = min(t1 - tt, int64_t(at.nt - at.i));
     const Run mine = run_of(at, tiles);
+    if (at.i == 0 && threadIdx.x == 0) {  // where this head's partials will be
+      // the range that holds tile x: (x + 1) n_ranges - 1 over total
+      const int64_t last = ((tt + at.nt) * n_ranges - 1) / total;
+      where[int64_t(b) * Hkv + g] =
+          make_int2(int(blockIdx.x) + b * Hkv + g, int(last) - int(blockIdx.x) + 1);
+    }
     tt += tiles;
     Q4State<NT> st;
     q4_init<NT>(st, q + (int64_t(b) * Hkv + g) * G * 128, G, scale_log2);
@@ -287,92 +293,109 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
       drain_phase(&full[warp][s], n_in > s ? (n_in - 1 - s) / STAGES + 1 : 0);
 }
 
-// grid (Hkv * G, B): the partials of (b, head) -> o, lse.  Each of MW warps
-// takes every MW-th partial, four dims per lane.
-constexpr int MW = NW;
-__global__ void __launch_bounds__(MW * 32)
-    decode_attn_q4_merge(const float2* __restrict__ part, const float* __restrict__ part_o,
-                         const __grid_constant__ Q4Lens lens, int B, int64_t cap, int Hkv, int G,
-                         int n_ctas, __nv_bfloat16* __restrict__ o, float* __restrict__ lse,
-                         float* __restrict__ lse2) {
-  __shared__ int s_pre[kQ4MaxBatch + 1];
-  __shared__ int s_sum[NW];
-  __shared__ float s_m[MW], s_l[MW];
-  __shared__ __align__(16) float s_o[MW][128];
-  const int h = blockIdx.x % G, g = blockIdx.x / G, b = blockIdx.y, lane = lane_id(), warp = warp_id();
-  tile_prefix(lens, B, cap, s_pre, s_sum);
-  const int64_t total = int64_t(s_pre[B]) * Hkv;
-  const int nt = s_pre[b + 1] - s_pre[b];
-  const int64_t head = int64_t(b) * Hkv * G + g * G + h;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (nt == 0) {  // an empty context
-    o[head * 128 + threadIdx.x] = __float2bfloat16_rn(0.f);
-    if (threadIdx.x == 0) {
-      if (lse != nullptr) lse[head] = -INFINITY;
-      if (lse2 != nullptr) lse2[head] = -INFINITY;
-    }
-    return;
-  }
-  const int64_t S = int64_t(s_pre[b]) * Hkv + int64_t(g) * nt;
-  // the range that holds tile x
-  const int64_t n_ranges = range_count(total, n_ctas);
-  auto cta_of = [&](int64_t x) { return ((x + 1) * n_ranges - 1) / total; };
-  const int64_t c0 = cta_of(S), c1 = cta_of(S + nt - 1);
-  const int64_t base = (c0 + int64_t(b) * Hkv + g) * G + h;
-  const int n = int(c1 - c0 + 1);
-  // running maximum, sum and output of this warp's partials, eight at a time
+// The partials of one head, `base + i * G` for i = first, first + step, ... < n,
+// joined by one warp, MU at a time: {m, l}, four dims per lane in acc.
+constexpr int MU = 16;
+__device__ __forceinline__ float2 join_partials(const float2* __restrict__ part,
+                                                const float* __restrict__ part_o, int64_t base, int G,
+                                                int first, int step, int n, float4& acc) {
+  const int lane = lane_id();
   float M = -INFINITY, L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int U = 8;
-  for (int i0 = warp; i0 < n; i0 += U * MW) {
-    float2 p[U];
-    float4 v[U];
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = first; i0 < n; i0 += MU * step) {
+    float2 p[MU];
+    float4 v[MU];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t at = base + int64_t(min(i0 + u * MW, n - 1)) * G;
-      p[u] = __ldcg(part + at);
-      v[u] = __ldcg(reinterpret_cast<const float4*>(part_o + at * 128) + lane);
-      if (i0 + u * MW >= n) p[u] = make_float2(-INFINITY, 0.f);
+    for (int u = 0; u < MU; ++u) {
+      p[u] = make_float2(-INFINITY, 0.f);
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + u * step < n) {
+        const int64_t at = base + int64_t(i0 + u * step) * G;
+        p[u] = __ldcg(part + at);
+        v[u] = __ldcg(reinterpret_cast<const float4*>(part_o + at * 128) + lane);
+      }
     }
     float m = M;
 #pragma unroll
-    for (int u = 0; u < U; ++u) m = fmaxf(m, p[u].x);
+    for (int u = 0; u < MU; ++u) m = fmaxf(m, p[u].x);
     const float keep = M == -INFINITY ? 0.f : fast_exp2(M - m);
     M = m;
     L *= keep;
     acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < MU; ++u) {
       const float w = p[u].x == -INFINITY ? 0.f : fast_exp2(p[u].x - M);
-      if (i0 + u * MW < n) {
-        L += p[u].y * w;
-        acc.x += v[u].x * w;
-        acc.y += v[u].y * w;
-        acc.z += v[u].z * w;
-        acc.w += v[u].w * w;
-      }
+      L += p[u].y * w;
+      acc.x += v[u].x * w;
+      acc.y += v[u].y * w;
+      acc.z += v[u].z * w;
+      acc.w += v[u].w * w;
     }
   }
-  *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = acc;
-  if (lane == 0) {
-    s_m[warp] = M;
-    s_l[warp] = L;
+  return make_float2(M, L);
+}
+
+// grid (Hkv * G / HC, B): the partials of HC heads of one KV head -> o, lse.  A
+// warp joins a head alone where it has few partials, the CTA's warps together
+// where it has many.
+template <int HC>
+__global__ void __launch_bounds__(NW * 32)
+    decode_attn_q4_merge(const float2* __restrict__ part, const float* __restrict__ part_o,
+                         const int2* __restrict__ where, const __grid_constant__ Q4Lens lens,
+                         int64_t cap, int Hkv, int G, __nv_bfloat16* __restrict__ o,
+                         float* __restrict__ lse, float* __restrict__ lse2) {
+  __shared__ float2 s_ml[NW];
+  __shared__ __align__(16) float s_o[NW][128];
+  const int per = G / HC, g = blockIdx.x / per, h0 = (blockIdx.x % per) * HC, b = blockIdx.y;
+  const int lane = lane_id(), warp = warp_id();
+  const int64_t pair = int64_t(b) * Hkv + g;
+  const bool empty = seq_length(lens, b, cap) == 0;
+  auto store = [&](int h, float2 ml, const float4& acc) {
+    const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;  // no context, or every logit -inf
+    const int64_t head = pair * G + h;
+    *reinterpret_cast<uint2*>(o + head * 128 + 4 * lane) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lane == 0) {
+      const float l2 = ml.y == 0.f ? -INFINITY : ml.x + __log2f(ml.y);
+      if (lse != nullptr) lse[head] = l2 * kLn2;
+      if (lse2 != nullptr) lse2[head] = l2;
+    }
+  };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (empty) {
+    for (int h = warp; h < HC; h += NW) store(h0 + h, make_float2(-INFINITY, 0.f), acc);
+    return;
   }
-  __syncthreads();
-  float m = -INFINITY, l = 0.f, a = 0.f;
-#pragma unroll
-  for (int w = 0; w < MW; ++w) m = fmaxf(m, s_m[w]);
-#pragma unroll
-  for (int w = 0; w < MW; ++w) {
-    const float f = s_m[w] == -INFINITY ? 0.f : fast_exp2(s_m[w] - m);
-    l += s_l[w] * f;
-    a += s_o[w][threadIdx.x] * f;
+  const int2 w = __ldcg(where + pair);
+  const int64_t base = int64_t(w.x) * G + h0;
+  if (w.y <= MU) {
+    for (int h = warp; h < HC; h += NW)
+      store(h0 + h, join_partials(part, part_o, base + h, G, 0, 1, w.y, acc), acc);
+    return;
   }
-  o[head * 128 + threadIdx.x] = __float2bfloat16_rn(l == 0.f ? 0.f : a / l);
-  if (threadIdx.x == 0) {
-    const float l2 = l == 0.f ? -INFINITY : m + __log2f(l);
-    if (lse != nullptr) lse[head] = l2 * kLn2;
-    if (lse2 != nullptr) lse2[head] = l2;
+  for (int h = 0; h < HC; ++h) {
+    s_ml[warp] = join_partials(part, part_o, base + h, G, warp, NW, w.y, acc);
+    *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = acc;
+    __syncthreads();
+    if (warp == h % NW) {
+      float M = -INFINITY, L = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < NW; ++i) M = fmaxf(M, s_ml[i].x);
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        const float f = s_ml[i].x == -INFINITY ? 0.f : fast_exp2(s_ml[i].x - M);
+        const float4 v = *reinterpret_cast<const float4*>(&s_o[i][4 * lane]);
+        L += s_ml[i].y * f;
+        acc.x += v.x * f;
+        acc.y += v.y * f;
+        acc.z += v.z * f;
+        acc.w += v.w * f;
+      }
+      store(h0 + h, make_float2(M, L), acc);
+    }
+    if (h + 1 < HC) __syncthreads();
   }
 }
 
@@ -530,36 +553,63 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
   }
 }
 
-template <int G, bool LOGITS>
-cudaError_t launch_attn_g(const Q4AttnArgs& a, cudaStream_t st) {
-  constexpr int NT = G > 8 ? G / 8 : 1;
-  const int64_t most = int64_t(a.B) * a.Hkv * ((a.cap + TILE - 1) / TILE);
-  constexpr int kMost = G > 8 ? kQ4AttnCtas * 2 / 3 : kQ4AttnCtas;  // one wave (launch bounds)
-  const int ctas = int(most < kMost ? most : kMost);
-  float2* part = reinterpret_cast<float2*>(a.ws);
-  const int64_t slots = int64_t(kQ4AttnCtas) + int64_t(a.B) * a.Hkv;
-  float* part_o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.ws) +
-                                           (size_t(slots) * G * 8 + 255) / 256 * 256);
-  const auto kernel = decode_attn_q4<G, LOGITS>;
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), attn_smem_bytes<NT>());
-  if (e != cudaSuccess) return e;
-  kernel<<<ctas, NW * 32, attn_smem_bytes<NT>(), st>>>(
-      reinterpret_cast<const __nv_bfloat16*>(a.q), a.cache, a.lens, a.B, a.cap, a.Hkv,
-      a.scale * kLog2e, a.logits, part, part_o);
+// workspace: partials' {m, l}, their outputs, and per (sequence, KV head) the
+// place and number of its partials
+struct AttnWs {
+  size_t o, where, bytes;
+};
+AttnWs attn_ws(int B, int Hkv, int G) {
+  const size_t slots = size_t(kQ4AttnCtas) + size_t(B) * Hkv;
+  auto r = [](size_t x) { return (x + 255) / 256 * 256; };
+  AttnWs w;
+  w.o = r(slots * G * sizeof(float2));
+  w.where = w.o + slots * G * 512;
+  w.bytes = w.where + r(size_t(B) * Hkv * sizeof(int2));
+  return w;
+}
+
+template <int HC>
+cudaError_t launch_merge(const Q4AttnArgs& a, const float2* part, const float* part_o,
+                         const int2* where, cudaStream_t st) {
   // the merge's CTAs may start while the last tiles are attended; they wait
   // for the whole grid before they read a partial
+  const int G = a.Hq / a.Hkv;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(a.Hkv) * G, unsigned(a.B));
-  cfg.blockDim = dim3(MW * 32);
+  cfg.gridDim = dim3(unsigned(a.Hq / HC), unsigned(a.B));
+  cfg.blockDim = dim3(NW * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, decode_attn_q4_merge, static_cast<const float2*>(part),
-                         static_cast<const float*>(part_o), a.lens, a.B, a.cap, a.Hkv, G, ctas,
-                         reinterpret_cast<__nv_bfloat16*>(a.o), a.lse, a.lse2);
+  return cudaLaunchKernelEx(&cfg, decode_attn_q4_merge<HC>, part, part_o, where, a.lens, a.cap, a.Hkv,
+                            G, reinterpret_cast<__nv_bfloat16*>(a.o), a.lse, a.lse2);
+}
+
+template <int G, bool LOGITS>
+cudaError_t launch_attn_g(const Q4AttnArgs& a, cudaStream_t st) {
+  constexpr int NT = G > 8 ? G / 8 : 1;
+  const int64_t most = int64_t(a.B) * a.Hkv * ((a.cap + TILE - 1) / TILE);
+  constexpr int kMost = G > 8 ? kQ4AttnCtas * 2 / 3 : kQ4AttnCtas;  // one wave (launch bounds)
+  const int ctas = int(most < kMost ? most : kMost);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(a.ws);
+  const AttnWs w = attn_ws(a.B, a.Hkv, G);
+  float2* part = reinterpret_cast<float2*>(ws);
+  float* part_o = reinterpret_cast<float*>(ws + w.o);
+  int2* where = reinterpret_cast<int2*>(ws + w.where);
+  const auto kernel = decode_attn_q4<G, LOGITS>;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), attn_smem_bytes<NT>());
+  if (e != cudaSuccess) return e;
+  kernel<<<ctas, NW * 32, attn_smem_bytes<NT>(), st>>>(
+      reinterpret_cast<const __nv_bfloat16*>(a.q), a.cache, a.lens, a.B, a.cap, a.Hkv,
+      a.scale * kLog2e, a.logits, part, part_o, where);
+  // a warp per head where there are many heads (their partials are few on
+  // average), a CTA per head where there are few
+  if (G >= 4 && int64_t(a.B) * a.Hq >= 4 * 148)
+    e = launch_merge<G >= 4 ? 4 : 1>(a, part, part_o, where, st);
+  else
+    e = launch_merge<1>(a, part, part_o, where, st);
   if (e != cudaSuccess) return e;
   count_launch(2);
   return cudaGetLastError();
@@ -612,10 +662,7 @@ cudaError_t launch_sparse_g(const Q4SparseArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-size_t attn_q4_workspace_bytes(int B, int Hq, int Hkv) {
-  const size_t G = Hq / Hkv, slots = size_t(kQ4AttnCtas) + size_t(B) * Hkv;
-  return (slots * G * 8 + 255) / 256 * 256 + slots * G * 512;
-}
+size_t attn_q4_workspace_bytes(int B, int Hq, int Hkv) { return attn_ws(B, Hkv, Hq / Hkv).bytes; }
 
 cudaError_t launch_attn_q4(const Q4AttnArgs& a, cudaStream_t st) {
   switch (a.Hq / a.Hkv) {
