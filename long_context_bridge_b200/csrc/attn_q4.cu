@@ -49,6 +49,10 @@ constexpr int attn_smem_bytes() {
   return NW * STAGES * STAGE_BYTES + int(sizeof(JoinBuf<NT>)) + 16;
 }
 
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 // The joined state of W warps for head h: {m, l}, four dims per lane in acc.
 template <int NT, int W>
 __device__ __forceinline__ float2 joined(const JoinBuf<NT, W>& join, int h, int lane, float4& acc) {
@@ -164,6 +168,7 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
   __shared__ int s_pre[kQ4MaxBatch + 1];
   __shared__ int s_sum[NW];
   __shared__ uint64_t full[NW][STAGES];
+  __shared__ __align__(16) __nv_bfloat16 s_q[2][G * 128];  // queries: this KV head's, the next one's
   extern __shared__ uint8_t dsmem_raw[];
   uint8_t* dsmem = dsmem_raw + ((16u - (smem_u32(dsmem_raw) & 15u)) & 15u);
   JoinBuf<NT>& join = *reinterpret_cast<JoinBuf<NT>*>(dsmem + NW * STAGES * STAGE_BYTES);
@@ -222,12 +227,18 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
     run.src += TILE * Q4_REC;
     ++n_in;
   };
+  auto fetch_q = [&](const TileAt& a, int buf) {
+    const __nv_bfloat16* src = q + (int64_t(a.b) * Hkv + a.g) * G * 128;
+    for (int i = threadIdx.x; i < G * 16; i += NW * 32) cp_async16(&s_q[buf][8 * i], src + 8 * i);
+  };
+  fetch_q(at, 0);
 #pragma unroll 1
   for (int s = 0; s < STAGES; ++s) fill();
 
+  int qbuf = 0;
   for (int64_t tt = t0; tt < t1;) {
     // ---- one (sequence, KV head): its tiles in this CTA's range
-    const int b = at.b, g = at.g;
+    const int b = at.b, g = at.g, i0 = at.i;
     const int64_t tiles = min(t1 - tt, int64_t(at.nt - at.i));
     const Run mine = run_of(at, tiles);
     if (at.i == 0 && threadIdx.x == 0) {  // where this head's partials will be
@@ -237,9 +248,16 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
           make_int2(int(blockIdx.x) + b * Hkv + g, int(last) - int(blockIdx.x) + 1);
     }
     tt += tiles;
+    // the head's queries have landed, and every warp is done with the last
+    // head's join buffer and queries; the next head's queries set out
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    next_head(at);
+    if (tt < t1) fetch_q(at, qbuf ^ 1);
     Q4State<NT> st;
-    q4_init<NT>(st, q + (int64_t(b) * Hkv + g) * G * 128, G, scale_log2);
-    float* lg = LOGITS ? logits + ((int64_t(b) * Hkv + g) * cap + at.i * TILE + warp * WT + gid) * G + 2 * t
+    q4_init<NT>(st, s_q[qbuf], G, scale_log2);
+    qbuf ^= 1;
+    float* lg = LOGITS ? logits + ((int64_t(b) * Hkv + g) * cap + i0 * TILE + warp * WT + gid) * G + 2 * t
                        : nullptr;
     int n = WT;  // records of the part being attended
     auto put = [&](int h, int nt, const float (&x)[4]) {
@@ -274,7 +292,6 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
       q4_step<NT, WT / 16, false, LOGITS>(st, arrive(), (1u << n) - 1, put);
       release();
     }
-    next_head(at);
     // ---- join the warps and write the partial
     q4_put<NT>(st, join.m[warp], join.l[warp], join.o[warp]);
     __syncthreads();
@@ -285,7 +302,6 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
       *reinterpret_cast<float4*>(part_o + (slot * G + h) * 128 + 4 * lane) = acc;
       if (lane == 0) part[slot * G + h] = ml;
     }
-    __syncthreads();
   }
   // after a wait that ran out: every copy that was issued lands before exit
   if (!ok && lane == 0)
@@ -405,10 +421,6 @@ __global__ void __launch_bounds__(NW * 32)
 constexpr int SK = 32;                     // records per stage
 constexpr int SST = 2;                     // stages per warp
 constexpr int SSTAGE_BYTES = SK * Q4_REC;  // 4608
-
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
 
 template <int NT, int W>
 constexpr int sparse_smem_bytes() {

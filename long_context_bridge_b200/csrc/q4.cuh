@@ -182,9 +182,9 @@ __device__ __forceinline__ float q4_inv_pow2(uint32_t bits) {
   return __uint_as_float(e < 254 ? (254 - e) << 23 : 0x00400000u);
 }
 
-// q: the G rows of 128 bf16 of this KV head's query heads
+// q: the G rows of 128 bf16 of this KV head's query heads (shared or global memory)
 template <int NT>
-__device__ __forceinline__ void q4_init(Q4State<NT>& st, const __nv_bfloat16* __restrict__ q, int G,
+__device__ __forceinline__ void q4_init(Q4State<NT>& st, const __nv_bfloat16* q, int G,
                                         float scale_log2) {
   const int lane = lane_id(), gid = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -194,7 +194,7 @@ __device__ __forceinline__ void q4_init(Q4State<NT>& st, const __nv_bfloat16* __
     uint32_t a = 0;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const uint4 v = hh < G ? __ldg(reinterpret_cast<const uint4*>(q + hh * 128 + 32 * g + 8 * t))
+      const uint4 v = hh < G ? *reinterpret_cast<const uint4*>(q + hh * 128 + 32 * g + 8 * t)
                              : make_uint4(0, 0, 0, 0);
       w[g][0] = v.x;
       w[g][1] = v.y;
@@ -206,6 +206,10 @@ __device__ __forceinline__ void q4_init(Q4State<NT>& st, const __nv_bfloat16* __
     }
     a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
     a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+    // in a vector register and unknown to the compiler (a < 2^15, but it comes
+    // from a shuffle): with two constants, or one in a uniform register, (x &
+    // mask) | magic takes two instructions, and the integer pipe bounds q4_step
+    st.magic = 0x64006400u | (a >> 15);
     // biased exponent of the head's largest |q|; 2^up brings it to [2^14, 2^15)
     const int e = int(a >> 7);
     const int up = e == 255 || a == 0 ? 0 : min(141 - e, 126);
@@ -245,9 +249,6 @@ __device__ __forceinline__ void q4_init(Q4State<NT>& st, const __nv_bfloat16* __
 #pragma unroll
     for (int i = 0; i < 8; ++i) st.o[nt][i][0] = st.o[nt][i][1] = st.o[nt][i][2] = st.o[nt][i][3] = 0.f;
   }
-  // as a value the compiler cannot see: with two constants, (x & mask) | magic
-  // became two instructions instead of one (the integer pipe bounds the step)
-  st.magic = __shfl_sync(0xffffffffu, 0x64006400u, 0);
   st.r_bits = 0x0080u;
   st.r_top = 0x00FF00FFu;
   st.r_inv = q4_inv_pow2(st.r_bits);
