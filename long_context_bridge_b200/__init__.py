@@ -321,12 +321,12 @@ def _on(t, dtype, what, dev):
     """Checked device pointer of a dense tensor on device index `dev`."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dtype is not dtype:
-        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        if t.dtype is not dtype:
+            raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+        if t.get_device() != dev:
+            raise ValueError(f"{what} is on cuda:{t.get_device()}, the cache on cuda:{dev}")
         raise ValueError(f"{what} must be contiguous")
-    if t.get_device() != dev:
-        raise ValueError(f"{what} is on cuda:{t.get_device()}, the cache on cuda:{dev}")
     return t.data_ptr()
 
 
@@ -342,7 +342,7 @@ def _run(fn, what, dev, stream, args):
         stream = torch._C._cuda_getCurrentRawStream(dev)  # .current_stream(dev).cuda_stream
     elif isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:  # the tensors' existence implies initialised CUDA
         status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -351,43 +351,43 @@ def _run(fn, what, dev, stream, args):
         raise HS2Error(status, what)
 
 
-def _rows(t, n_heads, what, dev):
+def _rows(t, n, n_heads, what, dev):
     """Pointer and token stride of K or V rows [n, n_kv_heads, 128] bf16, dense
     but for that stride."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
     if t.dtype is not BF16:
         raise ValueError(f"{what} must be {BF16}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != n_heads or t.shape[2] != 128:
-        raise ValueError(f"{what} must be [n, {n_heads}, 128], got {tuple(t.shape)}")
+    if t.shape != (n, n_heads, 128):
+        raise ValueError(f"{what} must be [{n}, {n_heads}, 128], got {tuple(t.shape)}")
     if t.get_device() != dev:
         raise ValueError(f"{what} is on cuda:{t.get_device()}, the cache on cuda:{dev}")
-    n = t.shape[0]
     ld, head, dim = t.stride()
     if n and (dim != 1 or (n_heads > 1 and head != 128)):
         raise ValueError(f"the heads of {what} must be dense (strides [ld, 128, 1])")
     return t.data_ptr(), ld if n > 1 else n_heads * 128
 
 
-def _row_args(K, V, slot, shape, dev):
-    k, ldk = _rows(K, shape.n_kv_heads, "K", dev)
-    v, ldv = _rows(V, shape.n_kv_heads, "V", dev)
-    n = K.shape[0]
-    if V.shape[0] != n or (slot is not None and slot.shape != (n,)):
-        raise ValueError("K, V and slot must hold the same number of tokens")
-    return k, v, ldk, ldv, None if slot is None else _on(slot, I32T, "slot", dev), n
+def _row_args(K, V, slot, n_heads, dev):
+    n = len(K)
+    k, ldk = _rows(K, n, n_heads, "K", dev)
+    v, ldv = _rows(V, n, n_heads, "V", dev)
+    if slot is not None:
+        if slot.shape != (n,):
+            raise ValueError(f"slot must be [{n}], got {tuple(slot.shape)}")
+        slot = _on(slot, I32T, "slot", dev)
+    return k, v, ldk, ldv, slot, n
 
 
 def _q4_cache(cache, shape):
     """Device index, pointer and batch of a 4-bit cache [batch, n_kv_heads, T, 144]."""
     if not isinstance(cache, torch.Tensor) or not cache.is_cuda:
         raise ValueError("cache must be a CUDA tensor")
-    dev = cache.get_device()
-    p = _on(cache, U8, "cache", dev)
-    if cache.dim() != 4 or cache.shape[1:] != (shape.n_kv_heads, shape.T, Q4_RECORD_BYTES):
+    dev, size = cache.get_device(), cache.shape
+    if len(size) != 4 or size[1:] != (shape.n_kv_heads, shape.T, Q4_RECORD_BYTES):
         raise ValueError(f"cache must be [batch, {shape.n_kv_heads}, {shape.T}, {Q4_RECORD_BYTES}],"
-                         f" got {tuple(cache.shape)}")
-    return dev, p, cache.shape[0]
+                         f" got {tuple(size)}")
+    return dev, _on(cache, U8, "cache", dev), size[0]
 
 
 def _fp8_cache(Kc, Vc, scales, shape):
@@ -410,7 +410,7 @@ def hs2_cache_write_q4(K, V, slot, cache, shape: Shape, first=0, stream=None):
     4-bit cache [batch, n_kv_heads, T, 144] at slot [n] int32, or (slot None)
     at first, first + 1, ...; see include/hs2.h."""
     dev, c, batch = _q4_cache(cache, shape)
-    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape, dev)
+    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape.n_kv_heads, dev)
     _run(_lib.hs2_cache_write_q4, "hs2_cache_write_q4", dev, stream,
          (k, v, ldk, ldv, sl, first, n, c, batch, C.byref(shape)))
 
@@ -419,7 +419,7 @@ def hs2_cache_read_q4(cache, slot, K, V, shape: Shape, first=0, stream=None):
     """Cache rows (slots as in hs2_cache_write_q4) as bf16 into K, V; a row
     whose slot is -1 stays as it was."""
     dev, c, batch = _q4_cache(cache, shape)
-    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape, dev)
+    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape.n_kv_heads, dev)
     _run(_lib.hs2_cache_read_q4, "hs2_cache_read_q4", dev, stream,
          (c, sl, first, n, k, v, ldk, ldv, batch, C.byref(shape)))
 
@@ -428,7 +428,7 @@ def hs2_cache_write_fp8(K, V, slot, Kc, Vc, scale, shape: Shape, first=0, stream
     """The e4m3 form of hs2_cache_write_q4: codes Kc, Vc [batch, T, n_kv_heads,
     128] and one fp32 scale per (token, KV head), the cache of hs2_block_decode."""
     dev, batch, ptrs = _fp8_cache(Kc, Vc, (scale,), shape)
-    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape, dev)
+    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape.n_kv_heads, dev)
     _run(_lib.hs2_cache_write_fp8, "hs2_cache_write_fp8", dev, stream,
          (k, v, ldk, ldv, sl, first, n, *ptrs, batch, C.byref(shape)))
 
@@ -436,7 +436,7 @@ def hs2_cache_write_fp8(K, V, slot, Kc, Vc, scale, shape: Shape, first=0, stream
 def hs2_cache_read_fp8(Kc, Vc, k_scale, v_scale, slot, K, V, shape: Shape, first=0, stream=None):
     """The e4m3 form of hs2_cache_read_q4."""
     dev, batch, ptrs = _fp8_cache(Kc, Vc, (k_scale, v_scale), shape)
-    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape, dev)
+    k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape.n_kv_heads, dev)
     _run(_lib.hs2_cache_read_fp8, "hs2_cache_read_fp8", dev, stream,
          (*ptrs, sl, first, n, k, v, ldk, ldv, batch, C.byref(shape)))
 
