@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
 
   const int warp = warp_id(), lane = lane_id(), gid = lane >> 2, t = lane & 3;
   uint8_t* ring = dsmem + warp * STAGES * STAGE_BYTES;
-  asm volatile("griddepcontrol.launch_dependents;");
+  grid_trigger();
   if (lane == 0) {
     for (int i = 0; i < STAGES; ++i) mbar_init(&full[warp][i], 1);
     fence_barrier_init();
@@ -359,13 +359,13 @@ __global__ void __launch_bounds__(NW * 32)
     decode_attn_q4_merge(const float2* __restrict__ part, const float* __restrict__ part_o,
                          const int2* __restrict__ where, const __grid_constant__ Q4Lens lens,
                          int64_t cap, int Hkv, int G, __nv_bfloat16* __restrict__ o,
-                         float* __restrict__ lse, float* __restrict__ lse2) {
+                         float* __restrict__ lse, float* __restrict__ lse2,
+                         uint32_t* __restrict__ zero, int n_zero) {
   __shared__ float2 s_ml[NW];
   __shared__ __align__(16) float s_o[NW][128];
   const int per = G / HC, g = blockIdx.x / per, h0 = (blockIdx.x % per) * HC, b = blockIdx.y;
   const int lane = lane_id(), warp = warp_id();
   const int64_t pair = int64_t(b) * Hkv + g;
-  const bool empty = seq_length(lens, b, cap) == 0;
   auto store = [&](int h, float2 ml, const float4& acc) {
     const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;  // no context, or every logit -inf
     const int64_t head = pair * G + h;
@@ -377,9 +377,14 @@ __global__ void __launch_bounds__(NW * 32)
       if (lse2 != nullptr) lse2[head] = l2;
     }
   };
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_wait();
+  grid_trigger();
+  if (zero != nullptr)  // the selection's counters, for the kernels that follow
+    for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * NW * 32 + threadIdx.x; i < n_zero;
+         i += gridDim.x * gridDim.y * NW * 32)
+      zero[i] = 0;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (empty) {
+  if (seq_length(lens, b, cap) == 0) {
     for (int h = warp; h < HC; h += NW) store(h0 + h, make_float2(-INFINITY, 0.f), acc);
     return;
   }
@@ -440,6 +445,7 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
               const int32_t* __restrict__ idx, float* __restrict__ lse, int64_t cap, int kw,
               float scale_log2) {
   constexpr int NT = G > 8 ? G / 8 : 1, W = NW;
+  grid_wait();
   // this CTA's joined state, read by the cluster's other CTAs
   __shared__ float2 c_ml[NT * 8];
   __shared__ __align__(16) float c_o[NT * 8][128];
@@ -586,17 +592,9 @@ cudaError_t launch_merge(const Q4AttnArgs& a, const float2* part, const float* p
   // the merge's CTAs may start while the last tiles are attended; they wait
   // for the whole grid before they read a partial
   const int G = a.Hq / a.Hkv;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(a.Hq / HC), unsigned(a.B));
-  cfg.blockDim = dim3(NW * 32);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_attn_q4_merge<HC>, part, part_o, where, a.lens, a.cap, a.Hkv,
-                            G, reinterpret_cast<__nv_bfloat16*>(a.o), a.lse, a.lse2);
+  return launch_dependent(decode_attn_q4_merge<HC>, dim3(unsigned(a.Hq / HC), unsigned(a.B)),
+                          dim3(NW * 32), 0, st, 1, part, part_o, where, a.lens, a.cap, a.Hkv, G,
+                          reinterpret_cast<__nv_bfloat16*>(a.o), a.lse, a.lse2, a.zero, a.n_zero);
 }
 
 template <int G, bool LOGITS>
@@ -633,24 +631,14 @@ cudaError_t launch_sparse_cs(const Q4SparseArgs& a, cudaStream_t st) {
   const auto kernel = sparse_q4<G, CS>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), sparse_smem_bytes<NT, W>());
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
   Q4Layers layers{};
   for (int l = 0; l < a.layers; ++l) {
     layers.q[l] = a.q[l];
     layers.o[l] = a.o[l];
   }
-  cfg.gridDim = dim3(unsigned(int64_t(a.B) * a.Hkv * CS), unsigned(a.layers));
-  cfg.blockDim = dim3(W * 32);
-  cfg.dynamicSmemBytes = sparse_smem_bytes<NT, W>();
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CS;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = CS > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kernel, layers, a.cache, a.idx, a.lse, a.cap, a.kw, a.scale * kLog2e);
+  const dim3 grid(unsigned(int64_t(a.B) * a.Hkv * CS), unsigned(a.layers));
+  e = launch_dependent(kernel, grid, dim3(W * 32), sparse_smem_bytes<NT, W>(), st, CS, layers, a.cache,
+                       a.idx, a.lse, a.cap, a.kw, a.scale * kLog2e);
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();

@@ -528,6 +528,8 @@ __global__ void __launch_bounds__(256)
                  uint32_t* __restrict__ done, int* __restrict__ kth_bucket) {
   __shared__ uint32_t sh[NBUCKET];
   __shared__ float sl[G];
+  grid_wait();
+  grid_trigger();
   const int c = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int N = seq_len.n[b];
   // candidates j <= i - w, i.e. j < N - w, inside the slice [lo, hi)
@@ -631,6 +633,8 @@ __global__ void __launch_bounds__(256)
   constexpr uint32_t LISTC = 1024;
   __shared__ uint2 s_list[LISTC];
   __shared__ uint32_t s_n, s_base;
+  grid_wait();
+  grid_trigger();
   const int c = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int N = seq_len.n[b];
   const int64_t s_lo = seq_len.lo[b];
@@ -829,6 +833,8 @@ __global__ void __launch_bounds__(512)
   __shared__ uint32_t s_hist[256];
   __shared__ uint32_t s_misc[4];
   __shared__ uint32_t s_wide[1024], s_pos[2048];  // k <= 2048
+  grid_wait();
+  grid_trigger();
   const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   const int N = seq_len.n[b];
   const int64_t i = N - 1;
@@ -1020,6 +1026,8 @@ cudaError_t launch_dec_g(const DecodeArgs& a, const SeqLens& d_seq, int max_len,
     q4.lse = a.lse;
     q4.lse2 = lse2;
     q4.logits = logits;
+    q4.zero = hist;  // histograms, counts and tickets
+    q4.n_zero = int(size_t(B) * Hkv * (NBUCKET + 2));
     q4.ws = ws_q4;
     e = launch_attn_q4(q4, st);
     if (e != cudaSuccess) return e;
@@ -1054,18 +1062,22 @@ cudaError_t launch_dec_g(const DecodeArgs& a, const SeqLens& d_seq, int max_len,
   }
   if (full || a.step == DEC_CP_SELECT) {
     // histograms, counts and tickets (adjacent: the histograms fill whole 256 bytes)
-    e = cudaMemsetAsync(hist, 0, size_t(B) * Hkv * (NBUCKET * 4 + 8), st);
-    if (e != cudaSuccess) return e;
+    if (a.cache4 == nullptr) {
+      e = cudaMemsetAsync(hist, 0, size_t(B) * Hkv * (NBUCKET * 4 + 8), st);
+      if (e != cudaSuccess) return e;
+    }
     if (nch_used > 0) {
       // keys per scoring CTA: 8192, or fewer (down to 1024) where that leaves
       // the GPU without four CTAs per SM
       int ch = CH;
       while (ch > 1024 && int64_t((max_len + ch - 1) / ch) * Hkv * B < 4 * 148) ch /= 2;
       const dim3 grid((max_len + ch - 1) / ch, Hkv, B);
-      decode_score<G><<<grid, 256, 0, st>>>(logits, lse2, d_seq, a.cap, Hkv, a.k, a.w, ch, score,
-                                            hist, done, kth_bucket);
-      decode_collect<<<grid, 256, 0, st>>>(score, kth_bucket, d_seq, a.cap, Hkv, a.k, a.w, ch, cand,
-                                           ccount);
+      e = launch_dependent(decode_score<G>, grid, dim3(256), 0, st, 1, logits, lse2, d_seq, a.cap, Hkv,
+                           a.k, a.w, ch, score, hist, done, kth_bucket);
+      if (e != cudaSuccess) return e;
+      e = launch_dependent(decode_collect, grid, dim3(256), 0, st, 1, score, kth_bucket, d_seq, a.cap,
+                           Hkv, a.k, a.w, ch, cand, ccount);
+      if (e != cudaSuccess) return e;
       launches += 2;
     }
     const int fsmem = CAPC * 8;
@@ -1076,8 +1088,9 @@ cudaError_t launch_dec_g(const DecodeArgs& a, const SeqLens& d_seq, int max_len,
       io.idx = a.idx;
       e = ensure_smem_attr(reinterpret_cast<const void*>(decode_final<FINAL_FULL>), fsmem);
       if (e != cudaSuccess) return e;
-      decode_final<FINAL_FULL><<<dim3(Hkv, B), 512, fsmem, st>>>(io, score, d_seq, a.cap, Hkv,
-                                                                 a.k, a.w);
+      e = launch_dependent(decode_final<FINAL_FULL>, dim3(Hkv, B), dim3(512), fsmem, st, 1, io, score,
+                           d_seq, a.cap, Hkv, a.k, a.w);
+      if (e != cudaSuccess) return e;
     } else {
       io.rec_out = a.sel_rec;
       e = ensure_smem_attr(reinterpret_cast<const void*>(decode_final<FINAL_LOCAL>), fsmem);
