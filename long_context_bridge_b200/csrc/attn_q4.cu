@@ -53,7 +53,8 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-// The joined state of W warps for head h: {m, l}, four dims per lane in acc.
+// The joined state of W warps for head h, in the form of q4_put: {log-sum-exp,
+// weight}, four dims of the normalised output per lane in acc.
 template <int NT, int W>
 __device__ __forceinline__ float2 joined(const JoinBuf<NT, W>& join, int h, int lane, float4& acc) {
   float M = -INFINITY, L = 0.f;
@@ -70,7 +71,10 @@ __device__ __forceinline__ float2 joined(const JoinBuf<NT, W>& join, int h, int 
     acc.z += v.z * w;
     acc.w += v.w * w;
   }
-  return make_float2(M, L);
+  if (L == 0.f) return make_float2(-INFINITY, 0.f);
+  const float n = 1.f / L;
+  acc = make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n);
+  return make_float2(M + __log2f(L), 1.f);
 }
 
 // length of sequence b, clamped to [0, cap]

@@ -249,8 +249,8 @@ __device__ __forceinline__ void q4_init(Q4State<NT>& st, const __nv_bfloat16* q,
 #pragma unroll
     for (int i = 0; i < 8; ++i) st.o[nt][i][0] = st.o[nt][i][1] = st.o[nt][i][2] = st.o[nt][i][3] = 0.f;
   }
-  st.r_bits = 0x0080u;
-  st.r_top = 0x00FF00FFu;
+  st.r_bits = (127 - 110) << 7;  // r2 >= 2^-110: p / r2 stays finite
+  st.r_top = (st.r_bits | 0x7Fu) * 0x00010001u;
   st.r_inv = q4_inv_pow2(st.r_bits);
 }
 
@@ -272,7 +272,9 @@ __device__ __forceinline__ void q4_raise(Q4State<NT>& st, const float (&s)[H][NT
       const float old = st.ref[nt][i], up = fmaxf(old, mx * st.f[nt][i] - 10.f);
       const float al = old == up ? 1.f : fast_exp2(old - up);
       st.ref[nt][i] = up;
-      st.top[nt][i] = (up + 14.f) / st.f[nt][i];
+      // below 14 by what the roundings of s * f and of this quotient can add, so
+      // that p stays below 2^14 for large logits too
+      st.top[nt][i] = (up + 14.f - fabsf(up) * 4.76837158e-7f) / st.f[nt][i];
       st.l[nt][i] *= al;
 #pragma unroll
       for (int d = 0; d < 8; ++d) {
@@ -436,9 +438,9 @@ __device__ __forceinline__ void q4_step(Q4State<NT>& st, const uint8_t* rec, uin
   }
 }
 
-// Joins the NW warps' states of a CTA.  Per head h < 8 NT: sM, sL (per warp)
-// and sO (times r2) in shared memory; the caller synchronises between this and
-// q4_joined.
+// One warp's state for the join: per head h < 8 NT the base-2 log-sum-exp sM
+// (-inf: no key), its weight sL (1, or 0 without a key) and the normalised
+// output sO, which stays within the range of V.
 template <int NT>
 __device__ __forceinline__ void q4_put(const Q4State<NT>& st, float* sM, float* sL,
                                        float (*sO)[128]) {
@@ -453,15 +455,16 @@ __device__ __forceinline__ void q4_put(const Q4State<NT>& st, float* sM, float* 
       for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
       const int h = nt * 8 + 2 * t + i;
       if (gid == 0) {
-        sM[h] = st.ref[nt][i];
-        sL[h] = l;
+        sM[h] = l == 0.f ? -INFINITY : st.ref[nt][i] + __log2f(l);
+        sL[h] = l == 0.f ? 0.f : 1.f;
       }
+      const float n = l == 0.f ? 0.f : r2 / l;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         // dims 32 g + 4 gid + {0, 1, 2, 3} = tiles 2g, 2g + 1, rows gid, gid + 8
         *reinterpret_cast<float4*>(&sO[h][32 * g + 4 * gid]) =
-            make_float4(st.o[nt][2 * g][i] * r2, st.o[nt][2 * g][i + 2] * r2,
-                        st.o[nt][2 * g + 1][i] * r2, st.o[nt][2 * g + 1][i + 2] * r2);
+            make_float4(st.o[nt][2 * g][i] * n, st.o[nt][2 * g][i + 2] * n,
+                        st.o[nt][2 * g + 1][i] * n, st.o[nt][2 * g + 1][i + 2] * n);
       }
     }
 }

@@ -101,7 +101,8 @@ def test_attention_long_context(hs2, Hq, H):
 
 
 @pytest.mark.parametrize("qmul,kmul,scale", [(1e-3, 1, None), (30, 3, None), (1e5, 1e-5, None),
-                                             (1e-30, 1e28, None), (1, 1, 4.0), (6, 2, 1.0)])
+                                             (1e-30, 1e28, None), (1, 1, 4.0), (6, 2, 1.0),
+                                             (300, 300, 1.0), (1e30, 1e-30, None)])
 def test_attention_magnitudes(hs2, qmul, kmul, scale):
     """Flat to one-hot softmax (logits up to thousands), large and small q and K."""
     lens = [515, 40]
@@ -129,6 +130,16 @@ def test_attention_rising_logits_and_v_scales(hs2):
     rec = ref.records(ref.to_bf16_bits(K), ref.to_bf16_bits(V))[None]
     o, lse = run_attn(hs2, rec, [n], Hq, q)
     check_attn(o, lse, q, rec, [n], Hq)
+
+
+@pytest.mark.parametrize("mul", [1e-35, 1e30, 2e37])
+def test_attention_v_over_the_whole_bf16_range(hs2, mul):
+    """V near the ends of bf16: sums of many tokens stay within V's range."""
+    lens = [3000, 17]
+    rec = make_cache(lens, 3000, 1, 55, vmul=lambda rng, s: mul)
+    q = rand_q(2, 8, 56)
+    o, lse = run_attn(hs2, rec, lens, 8, q)
+    check_attn(o, lse, q, rec, lens, 8)
 
 
 def test_attention_heads_with_zero_or_mixed_queries(hs2):
@@ -384,6 +395,45 @@ def test_block_decode(hs2, Hq, H, k, w, lens):
         x = torch.empty_like(o)
         hs2.hs2_sparse_attn_q4(qs[l], cache, idx, x, None, shape)
         assert torch.equal(x, os_[l])
+
+
+def test_captured_block_step(hs2):
+    """The captured step replays on new queries and cache contents, bit for bit
+    as the eager call, whatever the workspace held."""
+    import torch
+    lens, H, Hq, k, w, L = [900, 333], 2, 16, 128, 16, 3
+    cap = 900
+    shape = hs2.Shape.make(cap, Hq, H, k_global=k, window=w)
+    cache = torch.empty(2, H, cap, 144, dtype=torch.uint8, device="cuda")
+    q = torch.empty(2, Hq, 128, dtype=torch.bfloat16, device="cuda")
+    qs = [torch.empty_like(q) for _ in range(L)]
+    nb = hs2.workspace_size(hs2.OP_BLOCK_DECODE_Q4, shape, 2)
+    ws = torch.full((nb,), 0xFF, dtype=torch.uint8, device="cuda")
+
+    def outputs():
+        return (torch.empty_like(q), torch.empty(2, Hq, device="cuda"),
+                torch.empty(2, H, k + w, dtype=torch.int32, device="cuda"), [torch.empty_like(q) for _ in range(L)])
+
+    out = outputs()
+    g = torch.cuda.CUDAGraph()
+    cache.copy_(dev(make_cache(lens, cap, H, 1)))
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        hs2.hs2_block_decode_q4(lens, q, cache, out[0], out[1], out[2], qs, out[3], shape, ws)
+    for step in range(3):
+        cache.copy_(dev(make_cache(lens, cap, H, 500 + step)))
+        for i, t in enumerate([q, *qs]):
+            t.copy_(rand_q(2, Hq, 600 + 10 * step + i))
+        ws.fill_(255 - step)
+        for _ in range(2):
+            g.replay()
+        torch.cuda.synchronize()
+        want = outputs()
+        ws2 = torch.full((nb,), 7 * step, dtype=torch.uint8, device="cuda")
+        hs2.hs2_block_decode_q4(lens, q, cache, want[0], want[1], want[2], qs, want[3], shape, ws2)
+        for a, b in zip([*out[:3], *out[3]], [*want[:3], *want[3]]):
+            assert torch.equal(a, b)
+    assert hs2.hs2_get_device_status() == hs2.OK
 
 
 def test_serving_run(hs2):
