@@ -518,14 +518,11 @@ __global__ void __launch_bounds__(128)
 // ---------------------------------------------------------------------------
 // decode_score: grid (chunks of ch keys, Hkv, B), 256 threads
 // ---------------------------------------------------------------------------
-__device__ int block_kth_bucket(const uint32_t* __restrict__ gh, uint32_t k, uint32_t* s_scan);
-
 template <int G>
 __global__ void __launch_bounds__(256)
     decode_score(const float* __restrict__ logits, const float* __restrict__ lse2,
                  SeqLens seq_len, int64_t cap, int Hkv, int k, int w, int ch,
-                 float* __restrict__ score, uint32_t* __restrict__ hist,
-                 uint32_t* __restrict__ done, int* __restrict__ kth_bucket) {
+                 float* __restrict__ score, uint32_t* __restrict__ hist) {
   __shared__ uint32_t sh[NBUCKET];
   __shared__ float sl[G];
   grid_wait();
@@ -568,52 +565,37 @@ __global__ void __launch_bounds__(256)
   uint32_t* gh = hist + (size_t(b) * Hkv + g) * NBUCKET;
   for (int i = threadIdx.x; i < NBUCKET; i += 256)
     if (sh[i]) atomicAdd(&gh[i], sh[i]);
-  // the last CTA of (b, g) to finish finds the bucket of the k-th best score
-  __shared__ uint32_t s_last, s_scan[256];
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    s_last = atomicAdd(&done[size_t(b) * Hkv + g], 1u) == gridDim.x - 1;
-  }
-  __syncthreads();
-  if (s_last) {
-    __threadfence();
-    const int kb = block_kth_bucket(gh, uint32_t(k), s_scan);
-    if (threadIdx.x == 0) kth_bucket[size_t(b) * Hkv + g] = kb;
-  }
 }
 
 // bucket holding the k-th largest count from the top (NBUCKET bins, 256
-// threads); returns -1 if the total is below k
-__device__ int block_kth_bucket(const uint32_t* __restrict__ gh, uint32_t k, uint32_t* s_scan) {
-  // each thread sums 8 bins (highest first)
-  const int tid = threadIdx.x;
-  uint32_t c8[8], local = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    c8[i] = __ldcg(gh + NBUCKET - 1 - 8 * tid - i);  // other CTAs' atomics, from L2
-    local += c8[i];
-  }
-  s_scan[tid] = local;
-  __syncthreads();
-  // inclusive scan over 256 threads (simple Hillis-Steele)
-  for (int off = 1; off < 256; off <<= 1) {
-    const uint32_t v = tid >= off ? s_scan[tid - off] : 0u;
-    __syncthreads();
-    s_scan[tid] += v;
-    __syncthreads();
-  }
+// threads); -1 if the total is below k
+__device__ int block_kth_bucket(const uint32_t* __restrict__ gh, uint32_t k) {
+  __shared__ uint32_t s_sum[8];
   __shared__ int found;
+  const int tid = threadIdx.x, lane = lane_id(), warp = warp_id();
+  // thread t holds the eight bins below NBUCKET - 8 t, highest last
+  const uint4 lo = __ldcg(reinterpret_cast<const uint4*>(gh + NBUCKET - 8 - 8 * tid));
+  const uint4 hi = __ldcg(reinterpret_cast<const uint4*>(gh + NBUCKET - 4 - 8 * tid));
+  const uint32_t c8[8] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};
+  uint32_t local = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) local += c8[i];
+  uint32_t incl = local;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += v;
+  }
+  if (lane == 31) s_sum[warp] = incl;
   if (tid == 0) found = -1;
   __syncthreads();
-  const uint32_t incl = s_scan[tid], excl = incl - local;
+  for (int i = 0; i < warp; ++i) incl += s_sum[i];
+  const uint32_t excl = incl - local;
   if (excl < k && k <= incl) {
     uint32_t cum = excl;
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (cum + c8[i] >= k) {
-        found = NBUCKET - 1 - 8 * tid - i;
-        break;
-      }
+      if (cum < k && cum + c8[i] >= k) found = NBUCKET - 1 - 8 * tid - i;
       cum += c8[i];
     }
   }
@@ -625,8 +607,7 @@ __device__ int block_kth_bucket(const uint32_t* __restrict__ gh, uint32_t k, uin
 // decode_collect: grid (chunks of ch keys, Hkv, B), 256 threads
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256)
-    decode_collect(const float* __restrict__ score, const int* __restrict__ kth_bucket,
-                   SeqLens seq_len, int64_t cap, int Hkv, int k, int w, int ch,
+    decode_collect(const float* __restrict__ score, const uint32_t* __restrict__ hist, SeqLens seq_len, int64_t cap, int Hkv, int k, int w, int ch,
                    uint2* __restrict__ cand, uint32_t* __restrict__ ccount) {
   // candidates gather here first, so that a CTA takes its place in the (b, g)
   // list with one atomic
@@ -644,7 +625,7 @@ __global__ void __launch_bounds__(256)
   const int64_t j_hi = min(j_lo + ch, s_hi);
   if (j_lo >= j_hi) return;
   const size_t bg = size_t(b) * Hkv + g;
-  const int kb = kth_bucket[bg];
+  const int kb = block_kth_bucket(hist + bg * NBUCKET, uint32_t(k));
   const uint32_t thr = kb < 0 ? 0u : uint32_t(kb);
   const float* sc = score + bg * cap;  // score of key j at sc[j - s_lo]
   if (threadIdx.x == 0) s_n = 0;
@@ -1002,10 +983,7 @@ cudaError_t launch_dec_g(const DecodeArgs& a, const SeqLens& d_seq, int max_len,
   }
   float* lse2 = reinterpret_cast<float*>(take(size_t(B) * Hq * 4));
   uint32_t* hist = reinterpret_cast<uint32_t*>(take(size_t(B) * Hkv * NBUCKET * 4));
-  // per (b, g): candidate count, finished scoring CTAs, k-th best bucket
-  uint32_t* ccount = reinterpret_cast<uint32_t*>(take(size_t(B) * Hkv * 12));
-  uint32_t* done = ccount + size_t(B) * Hkv;
-  int* kth_bucket = reinterpret_cast<int*>(done + size_t(B) * Hkv);
+  uint32_t* ccount = reinterpret_cast<uint32_t*>(take(size_t(B) * Hkv * 4));  // candidates per (b, g)
   uint2* cand = reinterpret_cast<uint2*>(take(size_t(B) * Hkv * CAPC * 8));
   const float sl2 = a.scale * kLog2e;
   cudaError_t e = cudaSuccess;
@@ -1026,8 +1004,8 @@ cudaError_t launch_dec_g(const DecodeArgs& a, const SeqLens& d_seq, int max_len,
     q4.lse = a.lse;
     q4.lse2 = lse2;
     q4.logits = logits;
-    q4.zero = hist;  // histograms, counts and tickets
-    q4.n_zero = int(size_t(B) * Hkv * (NBUCKET + 2));
+    q4.zero = hist;  // histograms and counts, adjacent
+    q4.n_zero = int(size_t(B) * Hkv * (NBUCKET + 1));
     q4.ws = ws_q4;
     e = launch_attn_q4(q4, st);
     if (e != cudaSuccess) return e;
@@ -1061,9 +1039,9 @@ cudaError_t launch_dec_g(const DecodeArgs& a, const SeqLens& d_seq, int max_len,
     ++launches;
   }
   if (full || a.step == DEC_CP_SELECT) {
-    // histograms, counts and tickets (adjacent: the histograms fill whole 256 bytes)
+    // histograms and counts (adjacent: the histograms fill whole 256 bytes)
     if (a.cache4 == nullptr) {
-      e = cudaMemsetAsync(hist, 0, size_t(B) * Hkv * (NBUCKET * 4 + 8), st);
+      e = cudaMemsetAsync(hist, 0, size_t(B) * Hkv * (NBUCKET * 4 + 4), st);
       if (e != cudaSuccess) return e;
     }
     if (nch_used > 0) {
@@ -1073,9 +1051,9 @@ cudaError_t launch_dec_g(const DecodeArgs& a, const SeqLens& d_seq, int max_len,
       while (ch > 1024 && int64_t((max_len + ch - 1) / ch) * Hkv * B < 4 * 148) ch /= 2;
       const dim3 grid((max_len + ch - 1) / ch, Hkv, B);
       e = launch_dependent(decode_score<G>, grid, dim3(256), 0, st, 1, logits, lse2, d_seq, a.cap, Hkv,
-                           a.k, a.w, ch, score, hist, done, kth_bucket);
+                           a.k, a.w, ch, score, hist);
       if (e != cudaSuccess) return e;
-      e = launch_dependent(decode_collect, grid, dim3(256), 0, st, 1, score, kth_bucket, d_seq, a.cap,
+      e = launch_dependent(decode_collect, grid, dim3(256), 0, st, 1, score, hist, d_seq, a.cap,
                            Hkv, a.k, a.w, ch, cand, ccount);
       if (e != cudaSuccess) return e;
       launches += 2;
@@ -1189,7 +1167,7 @@ size_t dec_ws_bytes(int B, int64_t cap, int Hq, int Hkv, bool q4) {
   return r(size_t(B) * Hkv * cap * G * 4) + r(size_t(B) * Hkv * cap * 4) +
          (q4 ? r(attn_q4_workspace_bytes(B, Hq, Hkv))
              : r(size_t(B) * Hq * nch * sizeof(Partial)) + r(size_t(B) * Hq * nch * 128 * 4)) +
-         r(size_t(B) * Hq * 4) + r(size_t(B) * Hkv * NBUCKET * 4) + r(size_t(B) * Hkv * 12) +
+         r(size_t(B) * Hq * 4) + r(size_t(B) * Hkv * NBUCKET * 4) + r(size_t(B) * Hkv * 4) +
          r(size_t(B) * Hkv * CAPC * 8);
 }
 
