@@ -50,11 +50,11 @@ __device__ __forceinline__ int64_t token_slot(const int32_t* __restrict__ slot, 
   return -1;
 }
 
-// Index of slot s's record (s >= 0; -1 stays -1).
+// Byte offset of slot s's record (s >= 0; -1 stays -1).
 __device__ __forceinline__ int64_t record_of(int64_t s, const SlotDiv& d, int h, int Hkv) {
   if (s < 0) return -1;
   const uint32_t b = d.cap == 1 ? uint32_t(s) : __umulhi(uint32_t(s), d.mul) >> d.shift;
-  return (int64_t(b) * Hkv + h) * d.cap + (uint32_t(s) - b * d.cap);
+  return ((int64_t(b) * Hkv + h) * d.cap + (uint32_t(s) - b * d.cap)) * Q4_REC;
 }
 
 // largest |x| of a lane's eight bf16 values, as bf16 bits (a NaN ranks above
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(CW_WARPS * 32)
     if (is_v) w = wv;
     // the pair of groups (g, g ^ 1): the even one stores both scales
     const uint32_t s2 = __shfl_xor_sync(0xffffffffu, sc.bits, 4);
-    uint8_t* rec = cache + __shfl_sync(0xffffffffu, mine, u) * Q4_REC;
+    uint8_t* rec = cache + __shfl_sync(0xffffffffu, mine, u);
     if (!(live >> u & 1)) continue;
     reinterpret_cast<uint32_t*>(rec + (is_v ? Q4_V : Q4_K))[stored_word(is_v, g, t)] = w;
     if (t == 0 && (g & 1) == 0)
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(CW_WARPS * 32)
   uint32_t w[TOK], s[TOK];
 #pragma unroll
   for (int u = 0; u < TOK; ++u) {
-    const uint8_t* rec = cache + __shfl_sync(0xffffffffu, mine, u) * Q4_REC;
+    const uint8_t* rec = cache + __shfl_sync(0xffffffffu, mine, u);
     w[u] = s[u] = 0;
     if (live >> u & 1) {
       w[u] = __ldg(reinterpret_cast<const uint32_t*>(rec + (is_v ? Q4_V : Q4_K)) +

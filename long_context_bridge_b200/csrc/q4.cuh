@@ -74,10 +74,13 @@ __device__ __forceinline__ Q4Scale q4_scale(uint32_t a) {
 __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], const Q4Scale& s) {
   constexpr uint32_t kBase = 0x4B400000u;  // bits of 12582912
   uint32_t w = 0u - (kBase + (kBase << 4) + (kBase << 8));  // further shifts leave the word
+  const uint64_t inv = f2(s.inv, s.inv), snap = f2(6144.f, 6144.f),
+                 round = f2(12582920.f - 6144.f, 12582920.f - 6144.f);
 #pragma unroll
-  for (int n = 0; n < 8; ++n) {
-    const float q = __fadd_rn(__fmaf_rn(x[n], s.inv, 6144.f), 12582920.f - 6144.f);
-    w += __float_as_uint(q) << (4 * n);
+  for (int n = 0; n < 8; n += 2) {
+    float q0, q1;
+    f2_split(f2_add(f2_fma(f2(x[n], x[n + 1]), inv, snap), round), q0, q1);
+    w += (__float_as_uint(q0) << (4 * n)) + (__float_as_uint(q1) << (4 * n + 4));
   }
   return s.finite ? w : 0x88888888u;
 }
