@@ -9,13 +9,32 @@
 // tile and a ring of stages of its own, filled by untiled bulk copies of its
 // records (never past the sequence's length): no warp waits for another until
 // a (sequence, KV head) ends.  There the warps' states are joined and one
-// partial (m, l, o) is written; decode_attn_q4_merge joins the partials.
+// partial (log-sum-exp, normalised o) is written; decode_attn_q4_merge joins
+// the partials.
+//
+// What bounds it: with the arithmetic taken out the copies alone run at 6.6
+// TB/s; with it, two contexts of 1M tokens (32 / 4 heads, 1.18 GB) take 226 us =
+// 5.2 TB/s, 0.81 of the measured copy rate.  Per 16 tokens a warp issues about
+// 300 instructions, 145 of them on the integer pipe (one mask per pair of
+// codes), where HBM would leave an SM time for about 390 issue slots per
+// scheduler quarter; the integer pipe is 54% and the issue slots 59% busy, and
+// dependent latencies fill the rest.  Three CTAs of four warps per SM at 168
+// registers: two CTAs 286 us, four (128 registers, spills) 294 us where three
+// took 266; five warps per CTA 23% slower, six or seven 9% to 37%.  Steps of 32
+// keys rather than 16 (266 against 287 us) give the scheduler two independent
+// chains.  Tried and slower: the -8 of V's codes through a second MMA on a
+// constant operand (254 against 244 us), the shifts as multiply-high (247
+// against 228), q^T K as e4m3 MMAs with q split in two (291 against 228; the
+// legacy FP8 MMA is slow here), the queries' fragments in shared memory (equal
+// at 12 warps, 243 against 227 us at 16).
 //
 // sparse_q4: a cluster of CTAs per (sequence, KV head) splits the list; each
-// warp gathers sixteen records at a time into a ring of its own by 16-byte
+// warp gathers 32 records at a time into a ring of its own by 16-byte
 // asynchronous copies, and the cluster joins through distributed shared memory.
-// (One bulk copy per 144-byte record was limited by the rate at which an SM
-// starts bulk copies, about one per 20 cycles.)
+// One bulk copy per 144-byte record was limited by the rate at which an SM
+// starts bulk copies, about one per 20 cycles (300 x 4 lists of 1152: 100 us,
+// against 72 us).  Few lists are bound by latency (list entry -> record -> step
+// -> join), many by the same instructions as above.
 #include <cooperative_groups.h>
 
 #include "common.cuh"

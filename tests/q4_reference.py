@@ -95,9 +95,9 @@ def check(o, lse, q, rec, scale, what=""):
     """o [G, 128], lse [G] of the library against attend().
 
     o: half a bf16 step (2^-8) of its value, plus, relative to A = sum p |v|:
-    P rounded to f16 twice (2^-11 each), exp2 (2^-22) and logit errors ds of p
-    and of its sum, and a rounding of 2^-23 per accumulation (one per 16
-    tokens, and the joins).  Below 2^-24 f16 is absolute: 2^-35 of the running
+    two roundings of P to f16 (2^-11 each; the kernels round it once), exp2
+    (2^-22) and logit errors ds of p and of its sum, and a rounding of 2^-23 per
+    accumulation (one per 16 tokens, and the joins).  Below 2^-24 f16 is absolute: 2^-35 of the running
     maximum per token.  lse: ds, the sum's roundings, 2^-22 of exp2 and log2,
     and 2^-23 of its value for the last operations in fp32."""
     n = len(rec)
