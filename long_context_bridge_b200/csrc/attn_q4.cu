@@ -377,15 +377,15 @@ __device__ __forceinline__ float2 join_partials(const float2* __restrict__ part,
 // grid (Hkv * G / HC, B): the partials of HC heads of one KV head -> o, lse.  A
 // warp joins a head alone where it has few partials, the CTA's warps together
 // where it has many.
-template <int HC>
-__global__ void __launch_bounds__(NW * 32)
+template <int HC, int W>
+__global__ void __launch_bounds__(W * 32)
     decode_attn_q4_merge(const float2* __restrict__ part, const float* __restrict__ part_o,
                          const int2* __restrict__ where, const __grid_constant__ Q4Lens lens,
                          int64_t cap, int Hkv, int G, __nv_bfloat16* __restrict__ o,
                          float* __restrict__ lse, float* __restrict__ lse2,
                          uint32_t* __restrict__ zero, int n_zero) {
-  __shared__ float2 s_ml[NW];
-  __shared__ __align__(16) float s_o[NW][128];
+  __shared__ float2 s_ml[W];
+  __shared__ __align__(16) float s_o[W][128];
   const int per = G / HC, g = blockIdx.x / per, h0 = (blockIdx.x % per) * HC, b = blockIdx.y;
   const int lane = lane_id(), warp = warp_id();
   const int64_t pair = int64_t(b) * Hkv + g;
@@ -403,32 +403,32 @@ __global__ void __launch_bounds__(NW * 32)
   grid_wait();
   grid_trigger();
   if (zero != nullptr)  // the selection's counters, for the kernels that follow
-    for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * NW * 32 + threadIdx.x; i < n_zero;
-         i += gridDim.x * gridDim.y * NW * 32)
+    for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * W * 32 + threadIdx.x; i < n_zero;
+         i += gridDim.x * gridDim.y * W * 32)
       zero[i] = 0;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (seq_length(lens, b, cap) == 0) {
-    for (int h = warp; h < HC; h += NW) store(h0 + h, make_float2(-INFINITY, 0.f), acc);
+    for (int h = warp; h < HC; h += W) store(h0 + h, make_float2(-INFINITY, 0.f), acc);
     return;
   }
   const int2 w = __ldcg(where + pair);
   const int64_t base = int64_t(w.x) * G + h0;
   if (w.y <= MU) {
-    for (int h = warp; h < HC; h += NW)
+    for (int h = warp; h < HC; h += W)
       store(h0 + h, join_partials(part, part_o, base + h, G, 0, 1, w.y, acc), acc);
     return;
   }
   for (int h = 0; h < HC; ++h) {
-    s_ml[warp] = join_partials(part, part_o, base + h, G, warp, NW, w.y, acc);
+    s_ml[warp] = join_partials(part, part_o, base + h, G, warp, W, w.y, acc);
     *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = acc;
     __syncthreads();
-    if (warp == h % NW) {
+    if (warp == h % W) {
       float M = -INFINITY, L = 0.f;
       acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < NW; ++i) M = fmaxf(M, s_ml[i].x);
+      for (int i = 0; i < W; ++i) M = fmaxf(M, s_ml[i].x);
 #pragma unroll
-      for (int i = 0; i < NW; ++i) {
+      for (int i = 0; i < W; ++i) {
         const float f = s_ml[i].x == -INFINITY ? 0.f : fast_exp2(s_ml[i].x - M);
         const float4 v = *reinterpret_cast<const float4*>(&s_o[i][4 * lane]);
         L += s_ml[i].y * f;
@@ -461,12 +461,13 @@ struct Q4Layers {
   void* o[kQ4MaxLayers];
 };
 
-// grid (CS * pairs, layers)
+// grid (CS * pairs, layers): a pair is G query heads and the list that they
+// share with the split - 1 pairs beside it
 template <int G, int CS>
 __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
     sparse_q4(const __grid_constant__ Q4Layers layers, const uint8_t* __restrict__ cache,
               const int32_t* __restrict__ idx, float* __restrict__ lse, int64_t cap, int kw,
-              float scale_log2) {
+              int split, float scale_log2) {
   constexpr int NT = G > 8 ? G / 8 : 1, W = NW;
   grid_wait();
   // this CTA's joined state, read by the cluster's other CTAs
@@ -484,8 +485,8 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
   // this warp's entries [lo, hi) of the list, SK per step
   const int per = (kw + CS * W - 1) / (CS * W);
   const int lo = min(kw, (crank * W + warp) * per), hi = min(kw, lo + per);
-  const int32_t* list = idx + pair * kw;
-  const uint8_t* rows = cache + pair * cap * Q4_REC;
+  const int32_t* list = idx + pair / split * kw;
+  const uint8_t* rows = cache + pair / split * cap * Q4_REC;
   auto entry = [&](int step) {
     const int e = lo + step * SK + lane;
     return e < hi ? __ldg(list + e) : -1;
@@ -609,14 +610,14 @@ AttnWs attn_ws(int B, int Hkv, int G) {
   return w;
 }
 
-template <int HC>
+template <int HC, int W>
 cudaError_t launch_merge(const Q4AttnArgs& a, const float2* part, const float* part_o,
                          const int2* where, cudaStream_t st) {
   // the merge's CTAs may start while the last tiles are attended; they wait
   // for the whole grid before they read a partial
   const int G = a.Hq / a.Hkv;
-  return launch_dependent(decode_attn_q4_merge<HC>, dim3(unsigned(a.Hq / HC), unsigned(a.B)),
-                          dim3(NW * 32), 0, st, 1, part, part_o, where, a.lens, a.cap, a.Hkv, G,
+  return launch_dependent(decode_attn_q4_merge<HC, W>, dim3(unsigned(a.Hq / HC), unsigned(a.B)),
+                          dim3(W * 32), 0, st, 1, part, part_o, where, a.lens, a.cap, a.Hkv, G,
                           reinterpret_cast<__nv_bfloat16*>(a.o), a.lse, a.lse2, a.zero, a.n_zero);
 }
 
@@ -637,12 +638,17 @@ cudaError_t launch_attn_g(const Q4AttnArgs& a, cudaStream_t st) {
   kernel<<<ctas, NW * 32, attn_smem_bytes<NT>(), st>>>(
       reinterpret_cast<const __nv_bfloat16*>(a.q), a.cache, a.lens, a.B, a.cap, a.Hkv,
       a.scale * kLog2e, a.logits, part, part_o, where);
-  // a warp per head where there are many heads (their partials are few on
-  // average), a CTA per head where there are few
-  if (G >= 4 && int64_t(a.B) * a.Hq >= 4 * 148)
-    e = launch_merge<G >= 4 ? 4 : 1>(a, part, part_o, where, st);
+  // Many heads have few partials each on average: a warp per head.  Few heads
+  // may have hundreds (one context of 1M tokens, one KV head: 43 us with 16
+  // warps per head, 50 with 4), but 512 such CTAs take several waves (16 x 1000
+  // tokens, 32 heads: 20.8 us, 16.6 with 4).
+  const int64_t heads = int64_t(a.B) * a.Hq;
+  if (G >= 4 && heads >= 4 * 148)
+    e = launch_merge<G >= 4 ? 4 : 1, 4>(a, part, part_o, where, st);
+  else if (heads > 148)
+    e = launch_merge<1, 4>(a, part, part_o, where, st);
   else
-    e = launch_merge<1>(a, part, part_o, where, st);
+    e = launch_merge<1, 16>(a, part, part_o, where, st);
   if (e != cudaSuccess) return e;
   count_launch(2);
   return cudaGetLastError();
@@ -651,6 +657,7 @@ cudaError_t launch_attn_g(const Q4AttnArgs& a, cudaStream_t st) {
 template <int G, int CS>
 cudaError_t launch_sparse_cs(const Q4SparseArgs& a, cudaStream_t st) {
   constexpr int NT = G > 8 ? G / 8 : 1, W = NW;
+  const int split = a.Hq / a.Hkv / G;
   const auto kernel = sparse_q4<G, CS>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), sparse_smem_bytes<NT, W>());
   if (e != cudaSuccess) return e;
@@ -659,9 +666,9 @@ cudaError_t launch_sparse_cs(const Q4SparseArgs& a, cudaStream_t st) {
     layers.q[l] = a.q[l];
     layers.o[l] = a.o[l];
   }
-  const dim3 grid(unsigned(int64_t(a.B) * a.Hkv * CS), unsigned(a.layers));
+  const dim3 grid(unsigned(int64_t(a.B) * a.Hkv * split * CS), unsigned(a.layers));
   e = launch_dependent(kernel, grid, dim3(W * 32), sparse_smem_bytes<NT, W>(), st, CS, layers, a.cache,
-                       a.idx, a.lse, a.cap, a.kw, a.scale * kLog2e);
+                       a.idx, a.lse, a.cap, a.kw, split, a.scale * kLog2e);
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
@@ -670,16 +677,17 @@ cudaError_t launch_sparse_cs(const Q4SparseArgs& a, cudaStream_t st) {
 // How many CTAs share a list.  More of them shorten the chain of steps of a
 // warp, until the launch no longer fits the GPU at once (its second wave costs
 // as much as the first) or a warp's part falls below one step of 32 entries.
-// Measured, us: lists of 1152, G = 8: 32 lists 13.9 / 10.8 / 8.8 / 9.1 for 1 /
-// 2 / 4 / 8 CTAs, 64 lists 14.4 / 11.3 / 10.6 / 17.9, 256 lists 20.0 / 25.2 /
-// 32.5 / 50.8; one list of 2304, G = 16: 29.3 / 18.0 / 12.9 / 11.2; lists of
-// 128: 4.2 / 5.7 / 5.7 / 6.7.
+// Measured, us: lists of 1152, G = 8: 32 lists 13.7 / 10.8 / 9.3 / 9.3 for 1 /
+// 2 / 4 / 8 CTAs, 64 lists 13.9 / 11.3 / 10.4 / 18.0, 256 lists 19.1 / 25.2 /
+// 32.9 / 51.7; 32 lists of 2176 23.6 / 15.9 / 11.3 / 10.3; lists of 128: 4.2 /
+// 5.7 / 5.7 / 6.3.
 template <int G>
 cudaError_t launch_sparse_g(const Q4SparseArgs& a, cudaStream_t st) {
-  const int64_t pairs = int64_t(a.B) * a.Hkv * a.layers;  // lists x layers
-  if (pairs * 8 <= 148 && a.kw >= 8 * NW * SK) return launch_sparse_cs<G, 8>(a, st);
-  if (pairs * 4 <= 2 * 148 && a.kw >= 4 * NW * SK) return launch_sparse_cs<G, 4>(a, st);
-  if (pairs * 2 <= 2 * 148 && a.kw >= 2 * NW * SK) return launch_sparse_cs<G, 2>(a, st);
+  const int64_t pairs = int64_t(a.B) * a.Hq / G * a.layers;
+  const int64_t wave = G > 8 ? 2 * 148 : 3 * 148;  // CTAs (launch bounds)
+  if (pairs * 8 <= 2 * 148 && a.kw >= 8 * NW * SK) return launch_sparse_cs<G, 8>(a, st);
+  if (pairs * 4 <= wave && a.kw >= 4 * NW * SK) return launch_sparse_cs<G, 4>(a, st);
+  if (pairs * 2 <= wave && a.kw >= 2 * NW * SK) return launch_sparse_cs<G, 2>(a, st);
   return launch_sparse_cs<G, 1>(a, st);
 }
 
@@ -708,7 +716,13 @@ cudaError_t launch_sparse_q4(const Q4SparseArgs& a, cudaStream_t st) {
     case 2: return launch_sparse_g<2>(a, st);
     case 4: return launch_sparse_g<4>(a, st);
     case 8: return launch_sparse_g<8>(a, st);
-    case 16: return launch_sparse_g<16>(a, st);
+    case 16:
+      // Few lists: their heads in two pairs, twice the warps (one list of 2304
+      // 8.8 against 10.8 us, 16 lists 10.5 against 12.9, 96 lists 23.6 against
+      // 24.1).  Many: all heads together, each record unpacked once (128 lists
+      // 25.4 against 33.0 us).
+      if (int64_t(a.B) * a.Hkv * a.layers * 4 <= 3 * 148) return launch_sparse_g<8>(a, st);
+      return launch_sparse_g<16>(a, st);
     default: return cudaErrorInvalidValue;
   }
 }
