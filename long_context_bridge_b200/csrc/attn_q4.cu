@@ -91,7 +91,7 @@ __device__ __forceinline__ float2 joined(const JoinBuf<NT, W>& join, int h, int 
     acc.w += v.w * w;
   }
   if (L == 0.f) return make_float2(-INFINITY, 0.f);
-  const float n = 1.f / L;
+  const float n = __fdividef(1.f, L);
   acc = make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n);
   return make_float2(M + __log2f(L), 1.f);
 }
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(W * 32)
   const int lane = lane_id(), warp = warp_id();
   const int64_t pair = int64_t(b) * Hkv + g;
   auto store = [&](int h, float2 ml, const float4& acc) {
-    const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;  // no context, or every logit -inf
+    const float inv = ml.y == 0.f ? 0.f : __fdividef(1.f, ml.y);  // no context, or every logit -inf
     const int64_t head = pair * G + h;
     *reinterpret_cast<uint2*>(o + head * 128 + 4 * lane) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
   q4_put<NT>(st, join.m[warp], join.l[warp], join.o[warp]);
   __syncthreads();
   auto store = [&](int h, float2 ml, const float4& acc) {
-    const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;  // an empty list: o = 0, lse = -inf
+    const float inv = ml.y == 0.f ? 0.f : __fdividef(1.f, ml.y);  // an empty list: o = 0, lse = -inf
     const int64_t head = pair * G + h;
     *reinterpret_cast<uint2*>(O + head * 128 + 4 * lane) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));

@@ -461,13 +461,13 @@ __device__ __forceinline__ void q4_put(const Q4State<NT>& st, float* sM, float* 
         sM[h] = l == 0.f ? -INFINITY : st.ref[nt][i] + __log2f(l);
         sL[h] = l == 0.f ? 0.f : 1.f;
       }
-      const float n = l == 0.f ? 0.f : r2 / l;
+      const float n = l == 0.f ? 0.f : __fdividef(1.f, l);
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         // dims 32 g + 4 gid + {0, 1, 2, 3} = tiles 2g, 2g + 1, rows gid, gid + 8
         *reinterpret_cast<float4*>(&sO[h][32 * g + 4 * gid]) =
-            make_float4(st.o[nt][2 * g][i] * n, st.o[nt][2 * g][i + 2] * n,
-                        st.o[nt][2 * g + 1][i] * n, st.o[nt][2 * g + 1][i + 2] * n);
+            make_float4(st.o[nt][2 * g][i] * n * r2, st.o[nt][2 * g][i + 2] * n * r2,
+                        st.o[nt][2 * g + 1][i] * n * r2, st.o[nt][2 * g + 1][i + 2] * n * r2);
       }
     }
 }
