@@ -318,16 +318,19 @@ def hs2_decode_cp_finish(n_ranks, sparse_recs, o_sparse, shape: Shape, stream=No
 # short: pointers as plain ints, one pass of checks per tensor, and the device
 # is only switched when the tensors do not live on the current one.
 def _on(t, dtype, what, dev):
-    """Checked device pointer of a dense tensor on device index `dev`."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+    """Checked device pointer of a dense tensor on device index `dev` (a CPU
+    tensor's index is -1)."""
+    if isinstance(t, torch.Tensor):
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+        if not t.is_cuda:
+            raise ValueError(f"{what} must be a CUDA tensor")
         if t.dtype is not dtype:
             raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
         if t.get_device() != dev:
             raise ValueError(f"{what} is on cuda:{t.get_device()}, the cache on cuda:{dev}")
         raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{what} must be a CUDA tensor")
 
 
 def _shaped(t, shape, what):
@@ -354,18 +357,20 @@ def _run(fn, what, dev, stream, args):
 def _rows(t, n, n_heads, what, dev):
     """Pointer and token stride of K or V rows [n, n_kv_heads, 128] bf16, dense
     but for that stride."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dtype is not BF16:
-        raise ValueError(f"{what} must be {BF16}, got {t.dtype}")
-    if t.shape != (n, n_heads, 128):
+    if isinstance(t, torch.Tensor):
+        if t.dtype is BF16 and t.get_device() == dev and t.shape == (n, n_heads, 128):
+            ld, head, dim = t.stride()
+            if n == 0 or (dim == 1 and (head == 128 or n_heads == 1)):
+                return t.data_ptr(), ld if n > 1 else n_heads * 128
+            raise ValueError(f"the heads of {what} must be dense (strides [ld, 128, 1])")
+        if not t.is_cuda:
+            raise ValueError(f"{what} must be a CUDA tensor")
+        if t.dtype is not BF16:
+            raise ValueError(f"{what} must be {BF16}, got {t.dtype}")
+        if t.get_device() != dev:
+            raise ValueError(f"{what} is on cuda:{t.get_device()}, the cache on cuda:{dev}")
         raise ValueError(f"{what} must be [{n}, {n_heads}, 128], got {tuple(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{what} is on cuda:{t.get_device()}, the cache on cuda:{dev}")
-    ld, head, dim = t.stride()
-    if n and (dim != 1 or (n_heads > 1 and head != 128)):
-        raise ValueError(f"the heads of {what} must be dense (strides [ld, 128, 1])")
-    return t.data_ptr(), ld if n > 1 else n_heads * 128
+    raise ValueError(f"{what} must be a CUDA tensor")
 
 
 def _row_args(K, V, slot, n_heads, dev):
@@ -384,24 +389,27 @@ def _q4_cache(cache, shape):
     if not isinstance(cache, torch.Tensor) or not cache.is_cuda:
         raise ValueError("cache must be a CUDA tensor")
     dev, size = cache.get_device(), cache.shape
-    if len(size) != 4 or size[1:] != (shape.n_kv_heads, shape.T, Q4_RECORD_BYTES):
+    batch = size[0] if size else 0
+    if size != (batch, shape.n_kv_heads, shape.T, Q4_RECORD_BYTES):
         raise ValueError(f"cache must be [batch, {shape.n_kv_heads}, {shape.T}, {Q4_RECORD_BYTES}],"
                          f" got {tuple(size)}")
-    return dev, _on(cache, U8, "cache", dev), size[0]
+    return dev, _on(cache, U8, "cache", dev), batch
 
 
 def _fp8_cache(Kc, Vc, scales, shape):
     """Device index, batch and pointers of an e4m3 cache and its scales."""
     if not isinstance(Kc, torch.Tensor) or not Kc.is_cuda:
         raise ValueError("Kc must be a CUDA tensor")
-    dev, batch = Kc.get_device(), Kc.shape[0]
-    ptrs = [_on(Kc, U8, "Kc", dev), _on(Vc, U8, "Vc", dev)]
+    dev, size = Kc.get_device(), Kc.shape
+    batch = size[0] if size else 0
     rows = (batch, shape.T, shape.n_kv_heads)
-    _shaped(Kc, (*rows, 128), "Kc")
-    _shaped(Vc, (*rows, 128), "Vc")
+    codes = (*rows, 128)
+    _shaped(Kc, codes, "Kc")
+    _shaped(Vc, codes, "Vc")
+    ptrs = [_on(Kc, U8, "Kc", dev), _on(Vc, U8, "Vc", dev)]
     for s in scales:
-        ptrs.append(_on(s, F32, "scale", dev))
         _shaped(s, rows, "scale")
+        ptrs.append(_on(s, F32, "scale", dev))
     return dev, batch, ptrs
 
 

@@ -95,6 +95,8 @@ def test_binding_refusals(hs2):
         hs2.hs2_cache_write_q4(x, x, None, c, sh)
     with pytest.raises(ValueError, match="CUDA"):
         hs2.hs2_sparse_attn_q4(x, c, None, x, None, sh)
+    with pytest.raises(ValueError, match="CUDA"):
+        hs2.hs2_cache_read_fp8(None, c, x, x, None, x, x, sh)
 
 
 def test_reference_layout_is_a_permutation():
