@@ -101,7 +101,8 @@ __device__ __forceinline__ int seq_length(const Q4Lens& lens, int b, int64_t cap
   return lens.dev == nullptr ? lens.host[b] : min(max(__ldg(lens.dev + b), 0), int(cap));
 }
 
-// s_pre[b] = tiles of one KV head in sequences before b; s_pre[B] = all
+// s_pre[b] = tiles of one KV head in sequences before b; s_pre[B] = all (times
+// Hkv they fit an int: 2^31 tiles would be 39 TB of records)
 // (B <= kQ4MaxBatch, 128 threads, a CTA barrier on both sides)
 __device__ void tile_prefix(const Q4Lens& lens, int B, int64_t cap, int* s_pre, int* s_sum) {
   constexpr int PER = kQ4MaxBatch / (NW * 32);
@@ -146,18 +147,18 @@ struct TileAt {
   int b, g, i, nt, len;  // sequence, KV head, tile; that sequence's tiles and length
 };
 
-__device__ __forceinline__ TileAt tile_at(int64_t flat, const int* s_pre, const Q4Lens& lens,
+__device__ __forceinline__ TileAt tile_at(int flat, const int* s_pre, const Q4Lens& lens,
                                           int B, int64_t cap, int Hkv) {
   int lo = 0, hi = B;  // largest b with s_pre[b] * Hkv <= flat (its tiles not empty)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (int64_t(s_pre[mid]) * Hkv <= flat) lo = mid; else hi = mid;
+    if (s_pre[mid] * Hkv <= flat) lo = mid; else hi = mid;
   }
   TileAt a;
   a.b = lo;
   a.nt = s_pre[lo + 1] - s_pre[lo];
   a.len = seq_length(lens, lo, cap);
-  const int r = int(flat - int64_t(s_pre[lo]) * Hkv);
+  const int r = flat - s_pre[lo] * Hkv;
   a.g = r / a.nt;
   a.i = r - a.g * a.nt;
   return a;
@@ -174,12 +175,23 @@ __device__ __forceinline__ void tile_next(TileAt& a, const int* s_pre, const Q4L
   if (a.b < B) a.len = seq_length(lens, a.b, cap);
 }
 
-// Ranges that `total` tiles are cut into: range c is [total c / n, total (c +
-// 1) / n), none of them empty, so that the ranges of one (sequence, KV head)
-// are consecutive and each has written its partial.
-__device__ __forceinline__ int64_t range_count(int64_t total, int ctas) {
-  return total < ctas ? total : ctas;
-}
+// The equal ranges that `total` tiles are cut into: range c is [start(c),
+// start(c + 1)), none of them empty, so that the ranges of one (sequence, KV
+// head) are consecutive and each has written its partial.  An SM's three CTAs
+// do not end together (167, 191 and 215 us of 2 x 1M tokens: the first one
+// issues first), but shares of 9 : 8 : 7 in the order of launch made SMs end
+// apart instead (195 to 227 us), since that order does not tell which CTAs
+// share an SM; tiles drawn from a counter would make the order of the sums, and
+// with it the result's last bits, depend on timing.
+struct Cut {
+  int total, n;
+  __device__ Cut(int tiles, int ctas) : total(tiles), n(min(tiles, ctas)) {}
+  __device__ int start(int c) const { return int(uint64_t(total) * unsigned(c) / unsigned(n)); }
+  // the range that holds tile x: the last c with start(c) <= x
+  __device__ int of(int x) const {
+    return int((uint64_t(x + 1) * unsigned(n) - 1) / unsigned(total));
+  }
+};
 
 template <int G, bool LOGITS>
 __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
@@ -204,10 +216,9 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
     fence_barrier_init();
   }
   tile_prefix(lens, B, cap, s_pre, s_sum);  // its barriers publish the mbarriers too
-  const int64_t total = int64_t(s_pre[B]) * Hkv;
-  const int64_t n_ranges = range_count(total, gridDim.x);
-  if (blockIdx.x >= n_ranges) return;
-  const int64_t t0 = total * blockIdx.x / n_ranges, t1 = total * (blockIdx.x + 1) / n_ranges;
+  const Cut cut(s_pre[B] * Hkv, gridDim.x);
+  if (int(blockIdx.x) >= cut.n) return;
+  const int t0 = cut.start(blockIdx.x), t1 = cut.start(blockIdx.x + 1);
 
   // ---- this warp's records of a range: per (sequence, KV head) some whole
   // parts of WT records and at most one shorter one, copied in order
@@ -215,10 +226,10 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
     int whole, part;     // whole parts; records of the short one (0: none)
     const uint8_t* src;  // the first
   };
-  auto run_of = [&](const TileAt& a, int64_t tiles) {
+  auto run_of = [&](const TileAt& a, int tiles) {
     const int n = a.len - a.i * TILE - warp * WT;  // tokens from this warp's first part on
     Run r;
-    r.whole = min(int(tiles), n >= WT ? (n - WT) / TILE + 1 : 0);
+    r.whole = min(tiles, n >= WT ? (n - WT) / TILE + 1 : 0);
     r.part = r.whole < tiles ? max(0, min(WT - 1, n - r.whole * TILE)) : 0;
     r.src = cache + ((int64_t(a.b) * Hkv + a.g) * cap + int64_t(a.i) * TILE + warp * WT) * Q4_REC;
     return r;
@@ -228,14 +239,14 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
     tile_next(a, s_pre, lens, B, cap, Hkv);
   };
   TileAt at = tile_at(t0, s_pre, lens, B, cap, Hkv), ahead = at;
-  int64_t left = t1 - t0;  // tiles whose copies have not been reached
+  int left = t1 - t0;  // tiles whose copies have not been reached
   Run run{0, 0, nullptr};
   unsigned n_in = 0, n_out = 0;  // stages filled / attended so far
   bool ok = true;
   auto fill = [&]() {  // copies the next part
     while (run.whole == 0 && run.part == 0) {
       if (left == 0) return;
-      const int64_t tiles = min(left, int64_t(ahead.nt - ahead.i));
+      const int tiles = min(left, ahead.nt - ahead.i);
       run = run_of(ahead, tiles);
       left -= tiles;
       next_head(ahead);
@@ -259,16 +270,14 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
   for (int s = 0; s < STAGES; ++s) fill();
 
   int qbuf = 0;
-  for (int64_t tt = t0; tt < t1;) {
+  for (int tt = t0; tt < t1;) {
     // ---- one (sequence, KV head): its tiles in this CTA's range
     const int b = at.b, g = at.g, i0 = at.i;
-    const int64_t tiles = min(t1 - tt, int64_t(at.nt - at.i));
+    const int tiles = min(t1 - tt, at.nt - at.i);
     const Run mine = run_of(at, tiles);
     if (at.i == 0 && threadIdx.x == 0) {  // where this head's partials will be
-      // the range that holds tile x: (x + 1) n_ranges - 1 over total
-      const int64_t last = ((tt + at.nt) * n_ranges - 1) / total;
       where[int64_t(b) * Hkv + g] =
-          make_int2(int(blockIdx.x) + b * Hkv + g, int(last) - int(blockIdx.x) + 1);
+          make_int2(int(blockIdx.x) + b * Hkv + g, cut.of(tt + at.nt - 1) - int(blockIdx.x) + 1);
     }
     tt += tiles;
     // the head's queries have landed, and every warp is done with the last
