@@ -43,7 +43,7 @@ def awkward_rows(n, H, seed):
     return b
 
 
-CASES = [(1, 1, 8), (3, 2, 5), (4, 4, 7), (5, 2, 16), (17, 1, 40), (130, 4, 64), (1001, 8, 517)]
+CASES = [(1, 1, 1), (3, 2, 1), (7, 1, 2), (1, 1, 8), (3, 2, 5), (4, 4, 7), (5, 2, 16), (17, 1, 40), (130, 4, 64), (1001, 8, 517)]
 
 
 @pytest.mark.parametrize("n,H,cap", CASES)

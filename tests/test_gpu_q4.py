@@ -91,6 +91,24 @@ def test_attention_many_ragged_sequences(hs2):
     check_attn(o, lse, q, rec, lens, 8)
 
 
+def test_attention_largest_batch_and_workspace_bounds(hs2):
+    """512 sequences, a third of them idle, then all of them; nothing is written
+    behind a workspace of exactly the size asked for."""
+    import torch
+    rng = np.random.default_rng(4)
+    lens = np.where(rng.random(512) < 0.33, 0, rng.integers(1, 50, 512)).tolist()
+    rec = make_cache(lens, 50, 1, 23)
+    q = rand_q(512, 4, 24)
+    need = hs2.workspace_size(hs2.OP_DECODE_ATTN_Q4, hs2.Shape.make(50, 4, 1), 512)
+    buf = torch.full((need + 4096,), 0xAB, dtype=torch.uint8, device="cuda")
+    o, lse = run_attn(hs2, rec, lens, 4, q, ws=buf[:need])
+    check_attn(o, lse, q, rec, lens, 4)
+    o, lse = run_attn(hs2, rec, [0] * 512, 4, q, ws=buf[:need])
+    assert not o.any() and torch.isneginf(lse).all()
+    assert (buf[need:] == 0xAB).all()
+    assert hs2.hs2_get_device_status() == hs2.OK
+
+
 @pytest.mark.parametrize("Hq,H", [(8, 1), (16, 1)])
 def test_attention_long_context(hs2, Hq, H):
     lens = [70001, 333]
@@ -354,7 +372,8 @@ def reference_lists(q, rec, n, k, w):
 
 @pytest.mark.parametrize("Hq,H,k,w,lens", [(16, 2, 256, 64, [1500, 900, 320, 319, 64, 1]),
                                            (16, 1, 128, 16, [9001, 100]),
-                                           (4, 2, 64, 16, [700, 81, 80, 2]), (2, 2, 0, 16, [500, 3])])
+                                           (4, 2, 64, 16, [700, 81, 80, 2]), (2, 2, 0, 16, [500, 3]),
+                                           (8, 1, 2048, 32, [5000, 2081, 2080]), (1, 1, 1, 1, [3, 2, 1])])
 def test_block_decode(hs2, Hq, H, k, w, lens):
     import torch
     from helpers import SEL_REL
@@ -395,6 +414,49 @@ def test_block_decode(hs2, Hq, H, k, w, lens):
         x = torch.empty_like(o)
         hs2.hs2_sparse_attn_q4(qs[l], cache, idx, x, None, shape)
         assert torch.equal(x, os_[l])
+
+
+@pytest.mark.parametrize("k", [1, 100, 1024, 2048])
+def test_block_ties_take_the_smallest_positions(hs2, k):
+    """All records of a head equal, so every candidate's score ties: the list
+    holds positions 0 .. k - 1; and the workspace's end is respected."""
+    import torch
+    lens, H, Hq, w, cap = [4000, 2100], 2, 16, 16, 4000
+    rec = np.repeat(make_cache([1], 1, H, 7)[0][None, :, :1], cap, axis=2).repeat(2, 0)
+    shape = hs2.Shape.make(cap, Hq, H, k_global=k, window=w)
+    need = hs2.workspace_size(hs2.OP_BLOCK_DECODE_Q4, shape, 2)
+    buf = torch.full((need + 4096,), 0xAB, dtype=torch.uint8, device="cuda")
+    q = rand_q(2, Hq, 8)
+    o, lse = torch.empty_like(q), torch.empty(2, Hq, device="cuda")
+    idx = torch.empty(2, H, k + w, dtype=torch.int32, device="cuda")
+    hs2.hs2_block_decode_q4(lens, q, dev(rec), o, lse, idx, [], [], shape, buf[:need])
+    for b, n in enumerate(lens):
+        for g in range(H):
+            assert np.array_equal(idx[b, g].cpu().numpy(), np.r_[np.arange(min(k, n - w)),
+                                                                 np.full(max(0, k - (n - w)), -1),
+                                                                 np.arange(n - w, n)])
+    assert (buf[need:] == 0xAB).all()
+    check_attn(o, lse, q, rec, lens, Hq)
+
+
+def test_block_more_layers_than_one_launch_takes(hs2):
+    import torch
+    lens, H, Hq, k, w, L = [300, 40], 1, 8, 32, 8, 19
+    rec = make_cache(lens, 300, H, 9)
+    shape = hs2.Shape.make(300, Hq, H, k_global=k, window=w)
+    ws = torch.empty(hs2.workspace_size(hs2.OP_BLOCK_DECODE_Q4, shape, 2), dtype=torch.uint8, device="cuda")
+    cache, q = dev(rec), rand_q(2, Hq, 10)
+    qs = [rand_q(2, Hq, 11 + i) for i in range(L)]
+    os_ = [torch.empty_like(q) for _ in range(L)]
+    o, lse = torch.empty_like(q), torch.empty(2, Hq, device="cuda")
+    idx = torch.empty(2, H, k + w, dtype=torch.int32, device="cuda")
+    hs2.hs2_block_decode_q4(lens, q, cache, o, lse, idx, qs, os_, shape, ws)
+    gi = idx.cpu().numpy()
+    for i in range(L):
+        for b in range(2):
+            at = gi[b, 0][gi[b, 0] >= 0]
+            qh = host_f64(qs[i])[b]
+            ref.check(host_f64(os_[i])[b], ref.attend(qh, rec[b, 0, at], SC)[1], qh, rec[b, 0, at], SC)
 
 
 def test_captured_block_step(hs2):
