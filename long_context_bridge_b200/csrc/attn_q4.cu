@@ -541,8 +541,10 @@ __global__ void __launch_bounds__(NW * 32, G > 8 ? 2 : 3)
     const uint32_t k0 = keep[0];
     if (k0 == 0xFFFFFFFFu)
       q4_step<NT, SK / 16, true, false>(st, ring + s * SSTAGE_BYTES, k0, none);
-    else if (k0 != 0)
+    else if (k0 >> 16)
       q4_step<NT, SK / 16, false, false>(st, ring + s * SSTAGE_BYTES, k0, none);
+    else if (k0 != 0)  // a short last step: half the work
+      q4_step<NT, 1, false, false>(st, ring + s * SSTAGE_BYTES, k0, none);
     __syncwarp();  // every lane has read the stage
 #pragma unroll
     for (int u = 0; u + 1 < SST; ++u) keep[u] = keep[u + 1];
