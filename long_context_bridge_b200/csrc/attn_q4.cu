@@ -33,7 +33,7 @@
 // asynchronous copies, and the cluster joins through distributed shared memory.
 // One bulk copy per 144-byte record was limited by the rate at which an SM
 // starts bulk copies, about one per 20 cycles (300 x 4 lists of 1152: 100 us,
-// against 72 us).  Few lists are bound by latency (list entry -> record -> step
+// against 68 us).  Few lists are bound by latency (list entry -> record -> step
 // -> join), many by the same instructions as above.
 #include <cooperative_groups.h>
 
@@ -688,10 +688,10 @@ cudaError_t launch_sparse_cs(const Q4SparseArgs& a, cudaStream_t st) {
 // How many CTAs share a list.  More of them shorten the chain of steps of a
 // warp, until the launch no longer fits the GPU at once (its second wave costs
 // as much as the first) or a warp's part falls below one step of 32 entries.
-// Measured, us: lists of 1152, G = 8: 32 lists 13.7 / 10.8 / 9.3 / 9.3 for 1 /
-// 2 / 4 / 8 CTAs, 64 lists 13.9 / 11.3 / 10.4 / 18.0, 256 lists 19.1 / 25.2 /
-// 32.9 / 51.7; 32 lists of 2176 23.6 / 15.9 / 11.3 / 10.3; lists of 128: 4.2 /
-// 5.7 / 5.7 / 6.3.
+// Measured, us: lists of 1152, G = 8: 32 lists 13.4 / 10.3 / 8.7 / 8.5 for 1 /
+// 2 / 4 / 8 CTAs, 64 lists 13.4 / 10.3 / 9.8 / 16.5, 256 lists 18.5 / 23.6 /
+// 30.9 / 47.8; 32 lists of 2176 22.6 / 14.9 / 10.4 / 9.8; lists of 128: 4.2 /
+// 5.2 / 5.2 / 6.1.
 template <int G>
 cudaError_t launch_sparse_g(const Q4SparseArgs& a, cudaStream_t st) {
   const int64_t pairs = int64_t(a.B) * a.Hq / G * a.layers;

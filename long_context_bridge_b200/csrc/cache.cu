@@ -14,8 +14,8 @@
 //
 // Measured, written and read back (4 KV heads): a prompt of 128K tokens in
 // 4-bit records 125 us = 5.5 TB/s, 0.85 of the measured copy rate; 64K tokens
-// in e4m3 72 us = 5.6 TB/s, 0.87.  The quantiser issues about 115 instructions
-// per (token, head) and warp and keeps the issue slots 81% busy: scale, codes
+// in e4m3 72 us = 5.6 TB/s, 0.87.  The quantiser issues 114 instructions
+// per (token, head) and warp and keeps the issue slots 80% busy: scale, codes
 // and addresses without a division took it there from 213 us.
 #include "common.cuh"
 #include "kernels.h"
