@@ -13,8 +13,9 @@
 // the partials.
 //
 // What bounds it: with the arithmetic taken out the copies alone run at 6.6
-// TB/s; with it, two contexts of 1M tokens (32 / 4 heads, 1.18 GB) take 226 us =
-// 5.2 TB/s, 0.81 of the measured copy rate.  Per 16 tokens a warp issues about
+// TB/s; with it, two contexts of 1M tokens (32 / 4 heads, 1.18 GB) take 224 us =
+// 5.3 TB/s, 0.82 of the measured copy rate, in short bursts (258 us under
+// sustained load, where the power cap lowers the clock).  Per 16 tokens a warp issues about
 // 300 instructions, 145 of them on the integer pipe (one mask per pair of
 // codes), where HBM would leave an SM time for about 390 issue slots per
 // scheduler quarter; the integer pipe is 54% and the issue slots 59% busy, and
