@@ -2,7 +2,7 @@
 // each sequence's whole context (with its log-sum-exp, and for the block's
 // selection its logits), and over index lists (the sparse layers).
 //
-// decode_attn_q4: grid of kAttnCtas CTAs of four warps.  The contexts' tiles
+// decode_attn_q4: grid of at most kQ4AttnCtas CTAs of four warps.  The contexts' tiles
 // of 128 tokens, in the order (sequence, KV head, tile), are cut into equal
 // contiguous ranges, one per CTA, so ragged lengths leave no SM idle; every
 // CTA works out its range from the lengths.  Each warp owns 32 tokens of a
