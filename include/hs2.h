@@ -364,11 +364,12 @@ hs2_status hs2_cache_read_q4(const hs2_q4* cache, const int32_t* slot, int64_t f
  *   s_t = scale * q[b,h] . K^[b,g,t]   (0 <= t < seq_len[b])
  *   lse[b,h] = ln sum_t exp(s_t),  o[b,h] = sum_t exp(s_t - lse[b,h]) V^[b,g,t]
  * q, o [batch, n_q_heads, 128] bf16, |q| below 2^110; lse [batch, n_q_heads]
- * fp32.  seq_len: DEVICE int32 [batch], read when the call runs (a captured step replays with
- * the lengths of the moment); 0 is a batch row without context (o = 0,
- * lse = -inf), a length outside [0, shape->T] is taken as the nearest bound and
- * reported as HS2_ERR_BAD_INDEX.  What the cache holds from seq_len[b] on is
- * not read.  batch <= 512 (HS2_ERR_UNSUPPORTED otherwise).
+ * fp32.  The logits, taken to base 2, are held in fp32 and have to be finite
+ * there.  seq_len: DEVICE int32 [batch], read when the call runs (a captured
+ * step replays with the lengths of the moment); 0 is a batch row without
+ * context (o = 0, lse = -inf), a length outside [0, shape->T] is taken as the
+ * nearest bound and reported as HS2_ERR_BAD_INDEX.  What the cache holds from
+ * seq_len[b] on is not read.  batch <= 512 (HS2_ERR_UNSUPPORTED otherwise).
  * Workspace: hs2_workspace_size(HS2_OP_DECODE_ATTN_Q4, shape, batch, 0); it
  * need not be initialised and serves one call at a time.
  */

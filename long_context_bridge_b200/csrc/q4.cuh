@@ -157,7 +157,12 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 //
 // The softmax is base 2 against a reference `ref`: p = 2^(x - ref), with ref =
 // the running maximum - 10 and moved only when some x passes it by 14, so p
-// lies below 2^14 and the accumulators are rarely rescaled.
+// is at most 2^14 and the accumulators are rarely rescaled.  x is rounded to fp32
+// before ref is taken from it and subtracted, ref is rounded up and ref + 14
+// down: that holds for every finite x, also where fp32's spacing exceeds 14.
+// (With the product left exact in a fused multiply-add, half a spacing came on
+// top of the exponent, and from x = 2^27 on P left f16.  The multiplication of
+// its own costs one instruction per key and two heads.)
 //
 // O^T += V^T P^T: P times each group's V scale relative to `r2` (the power of
 // two at or below the largest V scale met so far) is rounded to f16 (2^-11
@@ -168,9 +173,9 @@ template <int NT>
 struct Q4State {
   uint32_t qf[NT][4][2][2];  // [group][MMA][register]
   float q8[NT][4][4];        // -8 * sum of the group's q * 2^-24, heads 2t, 2t+1, twice
-  float f[NT][2];            // logit (base 2) = f * scaled sum (f > 0)
+  float f[NT][2];            // logit x (base 2) = f * scaled sum, rounded (f > 0)
   float ref[NT][2], l[NT][2];
-  float top[NT][2];          // (ref + 14) / f: a scaled sum above it moves ref
+  float top[NT][2];          // ref + 14: a logit above it moves ref
   float o[NT][8][4];
   uint32_t r_bits;           // bf16 bits of r2
   uint32_t r_top;            // the largest bf16 below 2 r2, twice
@@ -258,26 +263,24 @@ __device__ __forceinline__ void q4_init(Q4State<NT>& st, const __nv_bfloat16* q,
 }
 
 // Moves the softmax references up to (maximum - 10) and r2 up to the largest
-// finite V scale's power of two; rescales what was accumulated.  s: the scaled
-// sums of 16 H keys; vs: V scales of the lane's 2 H keys.
+// finite V scale's power of two; rescales what was accumulated.  x: the base-2
+// logits of 16 H keys; vs: V scales of the lane's 2 H keys.
 template <int NT, int H>
-__device__ __forceinline__ void q4_raise(Q4State<NT>& st, const float (&s)[H][NT][4],
+__device__ __forceinline__ void q4_raise(Q4State<NT>& st, const float (&x)[H][NT][4],
                                          const uint2 (&vs)[H][2]) {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float mx = fmaxf(s[0][nt][i], s[0][nt][i + 2]);
+      float mx = fmaxf(x[0][nt][i], x[0][nt][i + 2]);
 #pragma unroll
-      for (int h = 1; h < H; ++h) mx = fmaxf(mx, fmaxf(s[h][nt][i], s[h][nt][i + 2]));
+      for (int h = 1; h < H; ++h) mx = fmaxf(mx, fmaxf(x[h][nt][i], x[h][nt][i + 2]));
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-      const float old = st.ref[nt][i], up = fmaxf(old, mx * st.f[nt][i] - 10.f);
+      const float old = st.ref[nt][i], up = fmaxf(old, __fadd_ru(mx, -10.f));
       const float al = old == up ? 1.f : fast_exp2(old - up);
       st.ref[nt][i] = up;
-      // below 14 by what the roundings of s * f and of this quotient can add, so
-      // that p stays below 2^14 for large logits too
-      st.top[nt][i] = (up + 14.f - fabsf(up) * 4.76837158e-7f) / st.f[nt][i];
+      st.top[nt][i] = __fadd_rd(up, 14.f);
       st.l[nt][i] *= al;
 #pragma unroll
       for (int d = 0; d < 8; ++d) {
@@ -364,18 +367,13 @@ __device__ __forceinline__ void q4_step(Q4State<NT>& st, const uint8_t* rec, uin
   for (int h = 0; h < H; ++h) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      if (!FULL) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!(keep >> (16 * h + gid + 8 * (i >> 1)) & 1)) s[h][nt][i] = -INFINITY;
+      for (int i = 0; i < 4; ++i) {
+        s[h][nt][i] = __fmul_rn(s[h][nt][i], st.f[nt][i & 1]);  // from here on the logit
+        if (!FULL && !(keep >> (16 * h + gid + 8 * (i >> 1)) & 1)) s[h][nt][i] = -INFINITY;
+        raise |= s[h][nt][i] > st.top[nt][i & 1];
       }
-      if (LOGITS) {
-        const float x[4] = {s[h][nt][0] * st.f[nt][0], s[h][nt][1] * st.f[nt][1],
-                            s[h][nt][2] * st.f[nt][0], s[h][nt][3] * st.f[nt][1]};
-        on_logits(h, nt, x);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) raise |= s[h][nt][i] > st.top[nt][i & 1];
+      if (LOGITS) on_logits(h, nt, s[h][nt]);
     }
     vmax = max_u16x2(vmax, max_u16x2(max_u16x2(vs[h][0].x, vs[h][0].y), max_u16x2(vs[h][1].x, vs[h][1].y)));
   }
@@ -399,7 +397,7 @@ __device__ __forceinline__ void q4_step(Q4State<NT>& st, const uint8_t* rec, uin
       float p[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        p[i] = fast_exp2(fmaf(s[h][nt][i], st.f[nt][i & 1], sub[nt][i & 1]));
+        p[i] = fast_exp2(s[h][nt][i] + sub[nt][i & 1]);
         st.l[nt][i & 1] += p[i];
         p[i] *= st.r_inv;
       }
