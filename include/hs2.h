@@ -393,7 +393,9 @@ hs2_status hs2_sparse_attn_q4(int32_t batch, const hs2_bf16* q, const hs2_q4* ca
 
 /*
  * hs2_block_decode over the 4-bit cache: the same step, arguments, limits and
- * outputs, with `cache` in place of the codes and scales.
+ * outputs, with `cache` in place of the codes and scales.  The sparse layers
+ * take effect in order, so a layer may read an earlier one's output as its
+ * queries (layers whose buffers do not overlap share a launch).
  * Workspace: hs2_workspace_size(HS2_OP_BLOCK_DECODE_Q4, shape, batch, 0).
  */
 hs2_status hs2_block_decode_q4(int32_t batch, const int64_t* seq_len, const hs2_bf16* q_full,

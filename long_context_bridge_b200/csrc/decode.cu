@@ -1099,14 +1099,23 @@ cudaError_t launch_dec_g(const DecodeArgs& a, const SeqLens& d_seq, int max_len,
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (a.cache4 != nullptr) {
-    // every layer's queries are there: the layers go together, a launch per
-    // kQ4MaxLayers of them
-    for (int l0 = 0; l0 < a.n_sparse; l0 += kQ4MaxLayers) {
+    // layers go together, up to kQ4MaxLayers in a launch, unless one of them
+    // reads or overwrites what an earlier one of the launch writes or reads: a
+    // caller may chain them (layer l's output as layer l + 1's queries)
+    const uintptr_t bytes = uintptr_t(B) * Hq * 256;
+    const auto meet = [&](const void* x, const void* y) {
+      const uintptr_t u = reinterpret_cast<uintptr_t>(x), v = reinterpret_cast<uintptr_t>(y);
+      return u < v + bytes && v < u + bytes;
+    };
+    for (int l0 = 0; l0 < a.n_sparse;) {
       Q4SparseArgs s{};
-      s.layers = std::min(kQ4MaxLayers, a.n_sparse - l0);
-      for (int l = 0; l < s.layers; ++l) {
-        s.q[l] = a.qs[l0 + l];
-        s.o[l] = a.os[l0 + l];
+      for (; l0 < a.n_sparse && s.layers < kQ4MaxLayers; ++l0) {
+        bool apart = true;
+        for (int l = 0; l < s.layers; ++l)
+          apart &= !meet(s.o[l], a.qs[l0]) && !meet(s.o[l], a.os[l0]) && !meet(s.q[l], a.os[l0]);
+        if (!apart) break;
+        s.q[s.layers] = a.qs[l0];
+        s.o[s.layers++] = a.os[l0];
       }
       s.cache = a.cache4;
       s.idx = a.idx;
