@@ -695,12 +695,15 @@ __device__ void block_bitonic_u64(uint64_t* s, int np, bool descending) {
     }
 }
 
-// The k largest of the n > k > 0 distinct keys s[0 .. n): radix select from the
-// highest bit in which they differ, ten bits a pass.  On return the keys x with
-// (x >> shift) >= (prefix >> shift) are the k largest.  512 threads.
+// The k largest of the n > k > 0 keys s[0 .. n): radix select from the highest
+// bit in which they differ, ten bits a pass.  On return the keys x with
+// (x >> shift) >= (prefix >> shift) are the k largest, or, where a key repeats
+// across the cut (records gathered twice; a context's own keys are distinct),
+// those above it and `copies` > 0 copies of the key `prefix`.  512 threads.
 struct KeyCut {
   uint64_t prefix;
   int shift;
+  uint32_t copies;
 };
 __device__ KeyCut block_top_k(const uint64_t* s, int n, uint32_t k, uint32_t* s_hist) {
   __shared__ uint64_t s_lo[16], s_hi[16];
@@ -726,7 +729,7 @@ __device__ KeyCut block_top_k(const uint64_t* s, int n, uint32_t k, uint32_t* s_
     lo = min(lo, s_lo[i]);
   }
   int top = 64 - __clzll(hi ^ lo);  // bits below this one are still open (n > 1: top >= 1)
-  KeyCut cut{top == 64 ? 0 : (hi >> top) << top, top};
+  KeyCut cut{top == 64 ? 0 : (hi >> top) << top, top, 0};
   while (true) {
     const int w = min(10, top), shift = top - w;
     const uint32_t mask = (1u << w) - 1;
@@ -759,7 +762,11 @@ __device__ KeyCut block_top_k(const uint64_t* s, int n, uint32_t k, uint32_t* s_
     cut.prefix |= uint64_t(s_pick[0]) << shift;
     cut.shift = top = shift;
     k = s_pick[1];
-    if (s_pick[2] == k || top == 0) return cut;  // the whole bin belongs to the k largest
+    if (s_pick[2] == k) return cut;  // the whole bin belongs to the k largest
+    if (top == 0) {                  // one key, s_pick[2] times
+      cut.copies = k;
+      return cut;
+    }
   }
 }
 
@@ -873,14 +880,16 @@ __global__ void __launch_bounds__(512)
     uint32_t* pos = s_pos;
     int kp = 1;
     while (kp < k) kp <<= 1;
-    KeyCut cut{0, 63};
+    KeyCut cut{0, 63, 0};
     if (n > uint32_t(k)) cut = block_top_k(sk, int(n), uint32_t(k), s_wide);
     if (tid == 0) s_misc[3] = 0;
     for (int e = k + tid; e < kp; e += blockDim.x) pos[e] = 0xFFFFFFFFu;
+    for (int e = tid; e < int(cut.copies); e += blockDim.x) pos[k - 1 - e] = ~uint32_t(cut.prefix);
     __syncthreads();
     for (int e0 = 0; e0 < int(n); e0 += blockDim.x) {
       const int e = e0 + tid;
-      const bool take = e < int(n) && (n <= uint32_t(k) || (sk[e] >> cut.shift) >= (cut.prefix >> cut.shift));
+      const bool take = e < int(n) && (n <= uint32_t(k) || (cut.copies > 0 ? sk[e] > cut.prefix
+                                                                           : (sk[e] >> cut.shift) >= (cut.prefix >> cut.shift)));
       const uint32_t bal = __ballot_sync(0xffffffffu, take);
       uint32_t at = 0;
       if (lane_id() == 0 && bal) at = atomicAdd(&s_misc[3], uint32_t(__popc(bal)));
