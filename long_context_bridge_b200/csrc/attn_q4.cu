@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(W * 32)
                          const int2* __restrict__ where, const __grid_constant__ Q4Lens lens,
                          int64_t cap, int Hkv, int G, __nv_bfloat16* __restrict__ o,
                          float* __restrict__ lse, float* __restrict__ lse2,
-                         uint32_t* __restrict__ zero, int n_zero) {
+                         uint32_t* __restrict__ zero, int64_t n_zero) {
   __shared__ float2 s_ml[W];
   __shared__ __align__(16) float s_o[W][128];
   const int per = G / HC, g = blockIdx.x / per, h0 = (blockIdx.x % per) * HC, b = blockIdx.y;
@@ -413,8 +413,8 @@ __global__ void __launch_bounds__(W * 32)
   grid_wait();
   grid_trigger();
   if (zero != nullptr)  // the selection's counters, for the kernels that follow
-    for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * W * 32 + threadIdx.x; i < n_zero;
-         i += gridDim.x * gridDim.y * W * 32)
+    for (int64_t i = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * W * 32 + threadIdx.x;
+         i < n_zero; i += int64_t(gridDim.x) * gridDim.y * W * 32)
       zero[i] = 0;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (seq_length(lens, b, cap) == 0) {

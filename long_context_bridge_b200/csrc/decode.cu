@@ -1014,7 +1014,7 @@ cudaError_t launch_dec_g(const DecodeArgs& a, const SeqLens& d_seq, int max_len,
     q4.lse2 = lse2;
     q4.logits = logits;
     q4.zero = hist;  // histograms and counts, adjacent
-    q4.n_zero = int(size_t(B) * Hkv * (NBUCKET + 1));
+    q4.n_zero = int64_t(B) * Hkv * (NBUCKET + 1);
     q4.ws = ws_q4;
     e = launch_attn_q4(q4, st);
     if (e != cudaSuccess) return e;

@@ -260,7 +260,7 @@ struct Q4AttnArgs {
   float* lse2;    // nullable, base 2
   float* logits;  // nullable: base-2 logits [B][Hkv][cap][G]
   uint32_t* zero;  // nullable: n_zero words to clear for the kernels that follow
-  int n_zero;
+  int64_t n_zero;
   void* ws;       // attn_q4_workspace_bytes
 };
 size_t attn_q4_workspace_bytes(int B, int Hq, int Hkv);

@@ -1,9 +1,11 @@
 """Calls over the 4-bit cache that the interface allows beyond the plain ones:
 buffers that layers share, other argument types, other launch shapes."""
+import numpy as np
 import pytest
 
-from helpers import dev
-from test_gpu_q4 import make_cache, rand_q
+import q4_reference as ref
+from helpers import dev, host_f64
+from test_gpu_q4 import SC, make_cache, rand_q
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +56,39 @@ def test_block_layers_that_share_buffers(hs2, B, Hq, H, k):
     hs2.hs2_sparse_attn_q4(want[half:half + B], cache, idx, o1, None, shape)
     assert torch.equal(buf, want) and torch.equal(last, o1)
     assert hs2.hs2_get_device_status() == hs2.OK
+
+
+def test_block_with_a_million_heads(hs2):
+    """2^20 (sequence, KV head) pairs, whose counters pass 2^31 words (the
+    workspace is 77 GB): every list holds its one best candidate, whatever the
+    workspace held."""
+    import torch
+    B, H, n, k, w = 64, 1 << 14, 3, 1, 1
+    shape = hs2.Shape.make(n, H, H, k_global=k, window=w)
+    need = hs2.workspace_size(hs2.OP_BLOCK_DECODE_Q4, shape, B)
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < need + (8 << 30):
+        pytest.skip("needs 86 GB of free device memory")
+    ws = torch.empty(need // 4, dtype=torch.int32, device="cuda").fill_(100)
+    rng = np.random.default_rng(3)
+    K, V = np.zeros((2, 128)), rng.standard_normal((2, 128))
+    K[0, 0], K[1, 0] = 2.0, -2.0                # the best candidate, every other key
+    rec = ref.records(ref.to_bf16_bits(K), ref.to_bf16_bits(V))
+    best = torch.randint(0, 2, (B, H), device="cuda", generator=torch.Generator("cuda").manual_seed(4))
+    mine = best[..., None] == torch.arange(n, device="cuda")
+    cache = torch.where(mine[..., None], dev(rec[0]), dev(rec[1]))
+    q = torch.zeros(B, H, 128, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    o, os_, lse = torch.empty_like(q), torch.empty_like(q), torch.empty(B, H, device="cuda")
+    idx = torch.empty(B, H, k + w, dtype=torch.int32, device="cuda")
+    hs2.hs2_block_decode_q4([n] * B, q, cache, o, lse, idx, [q], [os_], shape, ws.view(torch.uint8))
+    assert hs2.hs2_get_device_status() == hs2.OK
+    assert torch.equal(idx[..., 0].long(), best) and (idx[..., 1] == n - 1).all()
+    for c in range(2):      # all heads of one order of keys alike, the first one right
+        x, xs, l = o[best == c], os_[best == c], lse[best == c]
+        assert (x == x[0]).all() and (xs == xs[0]).all() and (l == l[0]).all()
+        qh, keys = host_f64(q[0, :1]), rec[[int(t != c) for t in range(n)]]
+        ref.check(host_f64(x[:1]), l[:1].double().cpu().numpy(), qh, keys, SC)
+        ref.check(host_f64(xs[:1]), ref.attend(qh, keys[[c, 2]], SC)[1], qh, keys[[c, 2]], SC)
+    del ws
+    torch.cuda.empty_cache()
