@@ -370,6 +370,10 @@ hs2_status hs2_cache_read_q4(const hs2_q4* cache, const int32_t* slot, int64_t f
  * context (o = 0, lse = -inf), a length outside [0, shape->T] is taken as the
  * nearest bound and reported as HS2_ERR_BAD_INDEX.  What the cache holds from
  * seq_len[b] on is not read.  batch <= 512 (HS2_ERR_UNSUPPORTED otherwise).
+ * o is accurate relative to the largest V^ of its own group of 32 dims in the
+ * context: exp(s_t - lse) times a key's V scale, over the largest exponential
+ * times the group's largest V scale, keeps 11 bits down to 2^-24 and an absolute
+ * 2^-35 below (a group's scales further apart than that lose the small ones).
  * Workspace: hs2_workspace_size(HS2_OP_DECODE_ATTN_Q4, shape, batch, 0); it
  * need not be initialised and serves one call at a time.
  */
@@ -384,7 +388,8 @@ hs2_status hs2_decode_attn_q4(int32_t batch, const int32_t* seq_len, const hs2_b
  * sequence b for its row.  idx [batch, n_kv_heads, k_global + window] holds
  * positions in [0, shape->T) of the row's own sequence, -1 skipped, any other
  * entry skipped and reported as HS2_ERR_BAD_INDEX; a position listed twice
- * counts twice.  An empty list: o = 0, lse = -inf.  lse nullable.  No
+ * counts twice.  An empty list: o = 0, lse = -inf.  Range and accuracy as
+ * hs2_decode_attn_q4 over the listed positions.  lse nullable.  No
  * workspace.  batch * n_kv_heads <= 2^28 - 1.
  */
 hs2_status hs2_sparse_attn_q4(int32_t batch, const hs2_bf16* q, const hs2_q4* cache,

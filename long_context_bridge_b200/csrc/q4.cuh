@@ -164,11 +164,13 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // top of the exponent, and from x = 2^27 on P left f16.  The multiplication of
 // its own costs one instruction per key and two heads.)
 //
-// O^T += V^T P^T: P times each group's V scale relative to `r2` (the power of
-// two at or below the largest V scale met so far) is rounded to f16 (2^-11
-// relative; below 2^-24 of the running maximum an absolute 2^-35 of it) where
-// the softmax has it, [key][head], and transposed by movmatrix into the B
-// fragment; V's codes are exact in f16.
+// O^T += V^T P^T: P times each group's V scale relative to the group's `r2` (the
+// power of two at or below the group's largest V scale met so far) is rounded to
+// f16 (2^-11 relative; below 2^-24 of the running maximum of P times the largest
+// scale an absolute 2^-35 of that) where the softmax has it, [key][head], and
+// transposed by movmatrix into the B fragment; V's codes are exact in f16.  A
+// reference per group keeps a group of small V beside one of large V; the
+// division by it is exact in bf16 and costs two instructions per key.
 template <int NT>
 struct Q4State {
   uint32_t qf[NT][4][2][2];  // [group][MMA][register]
@@ -177,17 +179,22 @@ struct Q4State {
   float ref[NT][2], l[NT][2];
   float top[NT][2];          // ref + 14: a logit above it moves ref
   float o[NT][8][4];
-  uint32_t r_bits;           // bf16 bits of r2
-  uint32_t r_top;            // the largest bf16 below 2 r2, twice
-  float r_inv;               // 1 / r2
+  uint32_t r_top[2];         // per group the largest bf16 below 2 r2 (two groups a word)
+  uint32_t r_inv[2];         // 1 / r2 as bf16
   uint32_t magic;            // 0x64006400 (see q4_step)
 };
 
 __device__ __forceinline__ float q4_pow2_bits(uint32_t bits) { return __uint_as_float(bits << 16); }
-// 1 / 2^(e - 127) for a power of two with biased exponent e in [1, 254]
-__device__ __forceinline__ float q4_inv_pow2(uint32_t bits) {
+// bf16 bits of 1 / 2^(e - 127) for those of a power of two with biased exponent e in [1, 254]
+__device__ __forceinline__ uint32_t q4_inv_pow2(uint32_t bits) {
   const uint32_t e = bits >> 7;
-  return __uint_as_float(e < 254 ? (254 - e) << 23 : 0x00400000u);
+  return e < 254 ? (254 - e) << 7 : 0x0040u;
+}
+// the lane's V scales of a key relative to the groups' references (exact)
+__device__ __forceinline__ uint32_t q4_scaled(uint32_t two, uint32_t inv) {
+  const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&two),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&inv));
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // q: the G rows of 128 bf16 of this KV head's query heads (shared or global memory)
@@ -257,13 +264,13 @@ __device__ __forceinline__ void q4_init(Q4State<NT>& st, const __nv_bfloat16* q,
 #pragma unroll
     for (int i = 0; i < 8; ++i) st.o[nt][i][0] = st.o[nt][i][1] = st.o[nt][i][2] = st.o[nt][i][3] = 0.f;
   }
-  st.r_bits = (127 - 110) << 7;  // r2 >= 2^-110: p / r2 stays finite
-  st.r_top = (st.r_bits | 0x7Fu) * 0x00010001u;
-  st.r_inv = q4_inv_pow2(st.r_bits);
+  constexpr uint32_t kLeast = (127 - 120) << 7;  // the least scale that is written
+  st.r_top[0] = st.r_top[1] = (kLeast | 0x7Fu) * 0x00010001u;
+  st.r_inv[0] = st.r_inv[1] = q4_inv_pow2(kLeast) * 0x00010001u;
 }
 
-// Moves the softmax references up to (maximum - 10) and r2 up to the largest
-// finite V scale's power of two; rescales what was accumulated.  x: the base-2
+// Moves the softmax references up to (maximum - 10) and each group's r2 up to its
+// largest finite V scale's power of two; rescales what was accumulated.  x: the base-2
 // logits of 16 H keys; vs: V scales of the lane's 2 H keys.
 template <int NT, int H>
 __device__ __forceinline__ void q4_raise(Q4State<NT>& st, const float (&x)[H][NT][4],
@@ -288,28 +295,30 @@ __device__ __forceinline__ void q4_raise(Q4State<NT>& st, const float (&x)[H][NT
         st.o[nt][d][i + 2] *= al;
       }
     }
-  uint32_t r = 0;
 #pragma unroll
-  for (int h = 0; h < H; ++h)
+  for (int g = 0; g < 4; ++g) {
+    const int sh = 16 * (g & 1);
+    uint32_t r = 0;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint32_t b[4] = {vs[h][u].x & 0xFFFFu, vs[h][u].x >> 16, vs[h][u].y & 0xFFFFu,
-                             vs[h][u].y >> 16};
+    for (int h = 0; h < H; ++h)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r = max(r, b[i] < 0x7F80u ? b[i] : 0u);
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t b = (g < 2 ? vs[h][u].x : vs[h][u].y) >> sh & 0xFFFFu;
+        r = max(r, b < 0x7F80u ? b : 0u);
+      }
+    r = __reduce_max_sync(0xffffffffu, r) & 0x7F80u;
+    const uint32_t old = st.r_top[g >> 1] >> sh & 0x7F80u;
+    if (r > old) {
+      const float al = q4_pow2_bits(old) * q4_pow2_bits(q4_inv_pow2(r));
+      st.r_top[g >> 1] = (st.r_top[g >> 1] & ~(0xFFFFu << sh)) | (r | 0x7Fu) << sh;
+      st.r_inv[g >> 1] = (st.r_inv[g >> 1] & ~(0xFFFFu << sh)) | q4_inv_pow2(r) << sh;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int d = 2 * g; d < 2 * g + 2; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st.o[nt][d][i] *= al;
     }
-  r = __reduce_max_sync(0xffffffffu, r) & 0x7F80u;
-  if (r > st.r_bits) {
-    const float al = q4_pow2_bits(st.r_bits) * q4_inv_pow2(r);
-    st.r_bits = r;
-    st.r_top = (r | 0x7Fu) * 0x00010001u;
-    st.r_inv = q4_inv_pow2(r);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int d = 0; d < 8; ++d)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) st.o[nt][d][i] *= al;
   }
 }
 
@@ -362,7 +371,7 @@ __device__ __forceinline__ void q4_step(Q4State<NT>& st, const uint8_t* rec, uin
   }
   // ---- does a reference have to move?
   bool raise = false;
-  uint32_t vmax = 0;
+  uint32_t vmax[2] = {0, 0};
 #pragma unroll
   for (int h = 0; h < H; ++h) {
 #pragma unroll
@@ -375,9 +384,11 @@ __device__ __forceinline__ void q4_step(Q4State<NT>& st, const uint8_t* rec, uin
       }
       if (LOGITS) on_logits(h, nt, s[h][nt]);
     }
-    vmax = max_u16x2(vmax, max_u16x2(max_u16x2(vs[h][0].x, vs[h][0].y), max_u16x2(vs[h][1].x, vs[h][1].y)));
+    vmax[0] = max_u16x2(vmax[0], max_u16x2(vs[h][0].x, vs[h][1].x));
+    vmax[1] = max_u16x2(vmax[1], max_u16x2(vs[h][0].y, vs[h][1].y));
   }
-  raise |= max_u16x2(vmax, st.r_top) != st.r_top;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) raise |= max_u16x2(vmax[i], st.r_top[i]) != st.r_top[i];
   if (__any_sync(0xffffffffu, raise)) q4_raise<NT, H>(st, s, vs);
   float sub[NT][2];  // no key yet: ref = -inf, every logit = -inf, p = 0
 #pragma unroll
@@ -389,8 +400,10 @@ __device__ __forceinline__ void q4_step(Q4State<NT>& st, const uint8_t* rec, uin
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     // ---- P' of each group, as B fragments [keys][head]
-    const float va[4] = {bf16lo(vs[h][0].x), bf16hi(vs[h][0].x), bf16lo(vs[h][0].y), bf16hi(vs[h][0].y)};
-    const float vb[4] = {bf16lo(vs[h][1].x), bf16hi(vs[h][1].x), bf16lo(vs[h][1].y), bf16hi(vs[h][1].y)};
+    const uint32_t v01 = q4_scaled(vs[h][0].x, st.r_inv[0]), v23 = q4_scaled(vs[h][0].y, st.r_inv[1]);
+    const uint32_t w01 = q4_scaled(vs[h][1].x, st.r_inv[0]), w23 = q4_scaled(vs[h][1].y, st.r_inv[1]);
+    const float va[4] = {bf16lo(v01), bf16hi(v01), bf16lo(v23), bf16hi(v23)};
+    const float vb[4] = {bf16lo(w01), bf16hi(w01), bf16lo(w23), bf16hi(w23)};
     uint32_t pb[NT][4][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -399,7 +412,6 @@ __device__ __forceinline__ void q4_step(Q4State<NT>& st, const uint8_t* rec, uin
       for (int i = 0; i < 4; ++i) {
         p[i] = fast_exp2(s[h][nt][i] + sub[nt][i & 1]);
         st.l[nt][i & 1] += p[i];
-        p[i] *= st.r_inv;
       }
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -446,7 +458,6 @@ template <int NT>
 __device__ __forceinline__ void q4_put(const Q4State<NT>& st, float* sM, float* sL,
                                        float (*sO)[128]) {
   const int lane = lane_id(), gid = lane >> 2, t = lane & 3;
-  const float r2 = q4_pow2_bits(st.r_bits);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -463,6 +474,7 @@ __device__ __forceinline__ void q4_put(const Q4State<NT>& st, float* sM, float* 
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         // dims 32 g + 4 gid + {0, 1, 2, 3} = tiles 2g, 2g + 1, rows gid, gid + 8
+        const float r2 = q4_pow2_bits(st.r_top[g >> 1] >> (16 * (g & 1)) & 0x7F80u);
         *reinterpret_cast<float4*>(&sO[h][32 * g + 4 * gid]) =
             make_float4(st.o[nt][2 * g][i] * n * r2, st.o[nt][2 * g][i + 2] * n * r2,
                         st.o[nt][2 * g + 1][i] * n * r2, st.o[nt][2 * g + 1][i + 2] * n * r2);

@@ -132,3 +132,64 @@ def test_random_large_logits(hs2, mul):
                 assert np.all(np.abs(o[0, h] - V[g, best]) <= O_REL * np.abs(V[g, best])), f"draw {seed} head {h}"
                 assert abs(lse[0, h] - s[best]) <= ds[best]
     assert apart >= draws * Hq      # of 2 * draws * Hq comparisons
+
+
+def check_groups(o, q, rec, scale, what):
+    """o [G, 128] against the definition, each group of 32 dims for itself: the
+    bound of q4_reference.check with the absolute term of f16's end taken from
+    the group alone.  A weight times a V scale loses at most 2^-25 (half of f16's
+    last spacing) of 2^10 (the least a largest weight stands at) times the
+    group's largest scale: 2^-35 of the group's largest |V| per key."""
+    want, _, A, ds = ref.attend(q, rec, scale)
+    V = ref.values(rec)[1]
+    n = len(rec)
+    rel = 2 * 2.0 ** -11 + 2 * (ds + 2.0 ** -22) + (n / 16 + 64) * 2.0 ** -23
+    for g in range(4):
+        d = slice(32 * g, 32 * g + 32)
+        tol = (2.0 ** -8 * np.abs(want[:, d]) + (1 + 2.0 ** -7) * rel[:, None] * A[:, d]
+               + n * 2.0 ** -35 * np.abs(V[:, d]).max())
+        assert np.median(tol / A[:, d]) < 2.0 ** -7, "the bound says nothing"
+        bad = np.abs(o[:, d] - want[:, d]) > tol
+        assert not bad.any(), f"{what}: group {g}, {bad.sum()} of {bad.size} off"
+
+
+@pytest.mark.parametrize("Hq,H", [(8, 1), (16, 1), (4, 2)])
+@pytest.mark.parametrize("powers", [(0, 20, 0, 0), (0, 60, -60, 5), (-110, 120, 0, 30), (-116, -100, -70, -40),
+                                    (122, 122, -116, 122)])
+def test_groups_of_v_far_apart(hs2, Hq, H, powers):
+    """Each group of 32 dims keeps its accuracy beside groups of any magnitude."""
+    n, G = 700, Hq // H
+    rng = np.random.default_rng(sum(abs(p) for p in powers))
+    K = rng.standard_normal((H, n, 128))
+    V = np.clip(rng.standard_normal((H, n, 128)), -3, 3) * np.repeat(np.exp2(np.array(powers, np.float64)), 32)
+    rec = ref.records(ref.to_bf16_bits(K), ref.to_bf16_bits(V))
+    qh = ref.from_bf16_bits(ref.to_bf16_bits(rng.standard_normal((1, Hq, 128))))
+    q = dev_bf16(ref.to_bf16_bits(qh))
+    sc = 128 ** -0.5
+    idx = np.tile(rng.permutation(n), (1, H, 1))
+    ob, _, lists, osb = block(hs2, rec[None], [n], q, sc, 300, 20)
+    for what, o in (("attention", attend(hs2, rec[None], [n], q, sc)[0]), ("list", sparse(hs2, rec[None], idx, q, sc)[0]),
+                    ("block", ob)):
+        for g in range(H):
+            h = slice(g * G, g * G + G)
+            check_groups(o[0, h], qh[0, h], rec[g], sc, what)
+    for g in range(H):
+        h = slice(g * G, g * G + G)
+        check_groups(osb[0, h], qh[0, h], rec[g, lists[0, g]], sc, "sparse layer")
+
+
+@pytest.mark.parametrize("spread", [8, 16, 22])
+def test_keys_of_v_far_apart(hs2, spread):
+    """V rows within 2^spread of each other in any order: the bound of a group
+    holds over all of its keys."""
+    n, Hq = 900, 8
+    rng = np.random.default_rng(spread)
+    K = rng.standard_normal((1, n, 128))
+    V = rng.standard_normal((1, n, 128)) * np.exp2(rng.uniform(-spread, 0, (1, n, 1)))
+    rec = ref.records(ref.to_bf16_bits(K), ref.to_bf16_bits(V))
+    qh = ref.from_bf16_bits(ref.to_bf16_bits(rng.standard_normal((1, Hq, 128))))
+    q = dev_bf16(ref.to_bf16_bits(qh))
+    sc = 128 ** -0.5
+    idx = rng.permutation(n)[None, None]
+    for what, o in (("attention", attend(hs2, rec[None], [n], q, sc)[0]), ("list", sparse(hs2, rec[None], idx, q, sc)[0])):
+        check_groups(o[0], qh[0], rec[0], sc, what)
