@@ -420,7 +420,7 @@ def hs2_cache_write_q4(K, V, slot, cache, shape: Shape, first=0, stream=None):
     dev, c, batch = _q4_cache(cache, shape)
     k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape.n_kv_heads, dev)
     _run(_lib.hs2_cache_write_q4, "hs2_cache_write_q4", dev, stream,
-         (k, v, ldk, ldv, sl, first, n, c, batch, C.byref(shape)))
+         (k, v, ldk, ldv, sl, int(first), n, c, batch, C.byref(shape)))
 
 
 def hs2_cache_read_q4(cache, slot, K, V, shape: Shape, first=0, stream=None):
@@ -429,7 +429,7 @@ def hs2_cache_read_q4(cache, slot, K, V, shape: Shape, first=0, stream=None):
     dev, c, batch = _q4_cache(cache, shape)
     k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape.n_kv_heads, dev)
     _run(_lib.hs2_cache_read_q4, "hs2_cache_read_q4", dev, stream,
-         (c, sl, first, n, k, v, ldk, ldv, batch, C.byref(shape)))
+         (c, sl, int(first), n, k, v, ldk, ldv, batch, C.byref(shape)))
 
 
 def hs2_cache_write_fp8(K, V, slot, Kc, Vc, scale, shape: Shape, first=0, stream=None):
@@ -438,7 +438,7 @@ def hs2_cache_write_fp8(K, V, slot, Kc, Vc, scale, shape: Shape, first=0, stream
     dev, batch, ptrs = _fp8_cache(Kc, Vc, (scale,), shape)
     k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape.n_kv_heads, dev)
     _run(_lib.hs2_cache_write_fp8, "hs2_cache_write_fp8", dev, stream,
-         (k, v, ldk, ldv, sl, first, n, *ptrs, batch, C.byref(shape)))
+         (k, v, ldk, ldv, sl, int(first), n, *ptrs, batch, C.byref(shape)))
 
 
 def hs2_cache_read_fp8(Kc, Vc, k_scale, v_scale, slot, K, V, shape: Shape, first=0, stream=None):
@@ -446,7 +446,7 @@ def hs2_cache_read_fp8(Kc, Vc, k_scale, v_scale, slot, K, V, shape: Shape, first
     dev, batch, ptrs = _fp8_cache(Kc, Vc, (k_scale, v_scale), shape)
     k, v, ldk, ldv, sl, n = _row_args(K, V, slot, shape.n_kv_heads, dev)
     _run(_lib.hs2_cache_read_fp8, "hs2_cache_read_fp8", dev, stream,
-         (*ptrs, sl, first, n, k, v, ldk, ldv, batch, C.byref(shape)))
+         (*ptrs, sl, int(first), n, k, v, ldk, ldv, batch, C.byref(shape)))
 
 
 def _workspace(ws, dev):
@@ -503,7 +503,7 @@ def hs2_block_decode_q4(seq_len, q_full, cache, o_full, lse, idx, q_sparse, o_sp
     _shaped(idx, (batch, shape.n_kv_heads, shape.k_global + shape.window), "idx")
     PP = C.POINTER(C.c_void_p)
     _run(_lib.hs2_block_decode_q4, "hs2_block_decode_q4", dev, stream,
-         (batch, (C.c_int64 * batch)(*seq_len), _on(q_full, BF16, "q_full", dev), c,
+         (batch, _i64s(seq_len), _on(q_full, BF16, "q_full", dev), c,
           _on(o_full, BF16, "o_full", dev), _on(lse, F32, "lse", dev), _on(idx, I32T, "idx", dev),
           layers, C.cast(qs, PP), C.cast(os_, PP), C.byref(shape), *_workspace(workspace, dev)))
 

@@ -92,3 +92,30 @@ def test_block_with_a_million_heads(hs2):
         ref.check(host_f64(xs[:1]), ref.attend(qh, keys[[c, 2]], SC)[1], qh, keys[[c, 2]], SC)
     del ws
     torch.cuda.empty_cache()
+
+
+def test_binding_takes_whole_numbers_of_any_kind(hs2):
+    """Lengths and first slots from numpy and torch as well as ints."""
+    import torch
+    lens, n, H, Hq, k, w = [120, 77], 120, 2, 8, 30, 8
+    shape = hs2.Shape.make(n, Hq, H, k_global=k, window=w)
+    cache, q = dev(make_cache(lens, n, H, 1)), rand_q(2, Hq, 2)
+    ws = torch.empty(hs2.workspace_size(hs2.OP_BLOCK_DECODE_Q4, shape, 2), dtype=torch.uint8, device="cuda")
+    outs = []
+    for kind in (list, np.array, torch.tensor, lambda x: np.array(x, np.int32), tuple):
+        o, lse, os_ = torch.empty_like(q), torch.empty(2, Hq, device="cuda"), torch.empty_like(q)
+        idx = torch.empty(2, H, k + w, dtype=torch.int32, device="cuda")
+        hs2.hs2_block_decode_q4(kind(lens), q, cache, o, lse, idx, [q], [os_], shape, ws)
+        outs.append((o, lse, idx, os_))
+    for x in outs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(x, outs[0]))
+    rows = torch.randn(3, H, 128, device="cuda").bfloat16()
+    for first in (np.int64(100), np.int32(100), torch.tensor(100)):
+        c = [torch.zeros_like(cache) for _ in range(2)]
+        hs2.hs2_cache_write_q4(rows, rows, None, c[0], shape, first=100)
+        hs2.hs2_cache_write_q4(rows, rows, None, c[1], shape, first=first)
+        assert c[0].any() and torch.equal(*c)
+        back = [torch.empty_like(rows) for _ in range(3)]
+        hs2.hs2_cache_read_q4(c[0], None, back[0], back[1], shape, first=first)
+        hs2.hs2_cache_read_q4(c[0], None, back[2], back[1], shape, first=100)
+        assert torch.equal(back[0], back[2])
