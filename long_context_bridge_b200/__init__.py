@@ -334,6 +334,8 @@ def _on(t, dtype, what, dev):
 
 
 def _shaped(t, shape, what):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{what} must be a CUDA tensor")
     if t.shape != shape:
         raise ValueError(f"{what} must be {shape}, got {tuple(t.shape)}")
 
@@ -374,12 +376,11 @@ def _rows(t, n, n_heads, what, dev):
 
 
 def _row_args(K, V, slot, n_heads, dev):
-    n = len(K)
+    n = len(K) if isinstance(K, torch.Tensor) and K.dim() else 0
     k, ldk = _rows(K, n, n_heads, "K", dev)
     v, ldv = _rows(V, n, n_heads, "V", dev)
     if slot is not None:
-        if slot.shape != (n,):
-            raise ValueError(f"slot must be [{n}], got {tuple(slot.shape)}")
+        _shaped(slot, (n,), "slot")
         slot = _on(slot, I32T, "slot", dev)
     return k, v, ldk, ldv, slot, n
 

@@ -119,3 +119,36 @@ def test_binding_takes_whole_numbers_of_any_kind(hs2):
         hs2.hs2_cache_read_q4(c[0], None, back[0], back[1], shape, first=first)
         hs2.hs2_cache_read_q4(c[0], None, back[2], back[1], shape, first=100)
         assert torch.equal(back[0], back[2])
+
+
+def test_binding_refuses_what_is_no_tensor(hs2):
+    """A missing or foreign argument is a ValueError, as everywhere in the binding."""
+    import torch
+    shape = hs2.Shape.make(16, 8, 2, k_global=3, window=1)
+    cache = torch.zeros(2, 2, 16, 144, dtype=torch.uint8, device="cuda")
+    Kc, S = torch.zeros(2, 16, 2, 128, dtype=torch.uint8, device="cuda"), torch.zeros(2, 16, 2, device="cuda")
+    x = torch.zeros(4, 2, 128, dtype=torch.bfloat16, device="cuda")
+    q, lse = torch.zeros(2, 8, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, 8, device="cuda")
+    n = torch.zeros(2, dtype=torch.int32, device="cuda")
+    idx = torch.zeros(2, 2, 4, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")
+    for bad in (lambda: hs2.hs2_cache_write_q4(None, x, None, cache, shape),
+                lambda: hs2.hs2_cache_write_q4(x, None, None, cache, shape),
+                lambda: hs2.hs2_cache_write_q4(x[0, 0, 0], x, None, cache, shape),
+                lambda: hs2.hs2_cache_write_q4(x, x, [0, 1, 2, 3], cache, shape),
+                lambda: hs2.hs2_cache_write_q4(x, x, None, None, shape),
+                lambda: hs2.hs2_cache_read_q4(cache, None, x, [x], shape),
+                lambda: hs2.hs2_cache_write_fp8(x, x, None, Kc, None, S, shape),
+                lambda: hs2.hs2_cache_write_fp8(x, x, None, Kc, Kc, None, shape),
+                lambda: hs2.hs2_cache_read_fp8(None, Kc, S, S, None, x, x, shape),
+                lambda: hs2.hs2_decode_attn_q4([1, 2], q, cache, q, lse, shape, ws),
+                lambda: hs2.hs2_decode_attn_q4(n, None, cache, q, lse, shape, ws),
+                lambda: hs2.hs2_decode_attn_q4(n, q, cache, q, None, shape, ws),
+                lambda: hs2.hs2_sparse_attn_q4(q, cache, None, q, None, shape),
+                lambda: hs2.hs2_block_decode_q4([1, 2], q, cache, q, lse, idx, [None], [q], shape, ws),
+                lambda: hs2.hs2_block_decode_q4([1, 2], q, cache, q, lse, None, [], [], shape, ws)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(hs2.HS2Error) as e:
+        hs2.hs2_decode_attn_q4(n, q, cache, q, lse, shape, None)
+    assert e.value.status == hs2.ERR_WORKSPACE
