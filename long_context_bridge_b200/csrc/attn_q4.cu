@@ -697,8 +697,10 @@ template <int G>
 cudaError_t launch_sparse_g(const Q4SparseArgs& a, cudaStream_t st) {
   const int64_t pairs = int64_t(a.B) * a.Hq / G * a.layers;
   const int64_t wave = G > 8 ? 2 * 148 : 3 * 148;  // CTAs (launch bounds)
-  if (pairs * 8 <= 2 * 148 && a.kw >= 8 * NW * SK) return launch_sparse_cs<G, 8>(a, st);
-  if (pairs * 4 <= wave && a.kw >= 4 * NW * SK) return launch_sparse_cs<G, 4>(a, st);
+  if constexpr (G <= 8) {  // 16 heads go together only where lists are many
+    if (pairs * 8 <= 2 * 148 && a.kw >= 8 * NW * SK) return launch_sparse_cs<G, 8>(a, st);
+    if (pairs * 4 <= wave && a.kw >= 4 * NW * SK) return launch_sparse_cs<G, 4>(a, st);
+  }
   if (pairs * 2 <= wave && a.kw >= 2 * NW * SK) return launch_sparse_cs<G, 2>(a, st);
   return launch_sparse_cs<G, 1>(a, st);
 }
