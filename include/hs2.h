@@ -340,7 +340,10 @@ hs2_status hs2_block_decode(int32_t batch, const int64_t* seq_len, const hs2_bf1
  *   A group that holds an infinity or a NaN: scale NaN, codes 0.
  *   Dim 32g + 8t + n of K (n < 8) is nibble 8(4t + g) + n; dim 32g + 4x + j of
  *   V (j < 4) is nibble 4(4x + g) + j; nibble 2i is the low half of byte i.
- * Read: bf16((nibble - 8) * scale).
+ * Read: bf16((nibble - 8) * scale).  A group whose amax is bf16's largest
+ * finite value, 0x7F7F, gets the scale 146/128 * 2^125: 7 * scale, finite in
+ * fp32, lies half way between that value and 2^128, and its bf16 is infinite.
+ * From 0x7F7E down every finite value reads back finite.
  */
 hs2_status hs2_cache_write_fp8(const hs2_bf16* K, const hs2_bf16* V, int64_t ldk, int64_t ldv,
                                const int32_t* slot, int64_t first, int64_t n, hs2_fp8e4m3* Kc,
