@@ -152,3 +152,59 @@ def test_binding_refuses_what_is_no_tensor(hs2):
     with pytest.raises(hs2.HS2Error) as e:
         hs2.hs2_decode_attn_q4(n, q, cache, q, lse, shape, None)
     assert e.value.status == hs2.ERR_WORKSPACE
+
+
+def test_captured_calls_behind_copies_and_joins(hs2):
+    """The dependent launches captured behind a copy, a memset, a join of two
+    streams and another call, replayed with new contents."""
+    import torch
+    B, n, H, Hq, k, w = 3, 500, 2, 16, 200, 30
+    shape = hs2.Shape.make(n, Hq, H, k_global=k, window=w)
+    cache = torch.zeros(B, H, n, 144, dtype=torch.uint8, device="cuda")
+    src, q = torch.zeros_like(cache), torch.zeros(B, Hq, 128, dtype=torch.bfloat16, device="cuda")
+    idx = torch.zeros(B, H, k + w, dtype=torch.int32, device="cuda")
+    idx_src = torch.zeros_like(idx)
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    o = [torch.zeros_like(q) for _ in range(5)]
+    lse = [torch.zeros(B, Hq, device="cuda") for _ in range(5)]
+    rows = torch.zeros(B, 2 * H, 128, dtype=torch.bfloat16, device="cuda")
+    slot = torch.tensor([b * n + 3 for b in range(B)], dtype=torch.int32, device="cuda")
+    ws = torch.empty(hs2.workspace_size(hs2.OP_DECODE_ATTN_Q4, shape, B), dtype=torch.uint8, device="cuda")
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=main):
+        cache.copy_(src)                                        # behind a copy
+        hs2.hs2_decode_attn_q4(lens, q, cache, o[0], lse[0], shape, ws)
+        idx.copy_(idx_src)
+        hs2.hs2_sparse_attn_q4(q, cache, idx, o[1], lse[1], shape)
+        side.wait_stream(main)                                  # two branches that join
+        with torch.cuda.stream(side):
+            hs2.hs2_cache_write_q4(rows[:, :H], rows[:, H:], slot, cache, shape)
+        hs2.hs2_sparse_attn_q4(o[1], src, idx, o[2], lse[2], shape)
+        main.wait_stream(side)
+        hs2.hs2_sparse_attn_q4(o[2], cache, idx, o[3], lse[3], shape)
+        idx.zero_()                                             # behind a memset
+        hs2.hs2_sparse_attn_q4(q, cache, idx, o[4], lse[4], shape)
+    for step in range(3):
+        rec = make_cache([n] * B, n, H, 30 + step)
+        src.copy_(dev(rec))
+        q.copy_(rand_q(B, Hq, 40 + step))
+        rng = np.random.default_rng(step)
+        idx_src.copy_(dev(np.stack([rng.permutation(n)[:k + w] for _ in range(B * H)]).astype(np.int32)).view(B, H, -1))
+        rows.copy_(rand_q(B, 2 * H, 50 + step))
+        lens.copy_(torch.tensor([n - step, step, 1]))
+        g.replay()
+        torch.cuda.synchronize()
+        full = src.clone()
+        x, y = torch.empty_like(q), torch.empty(B, Hq, device="cuda")
+        hs2.hs2_decode_attn_q4(lens, q, full, x, y, shape, torch.full_like(ws, 255), stream=0)
+        assert torch.equal(x, o[0]) and torch.equal(y, lse[0])
+        for i, (a, c, at) in enumerate([(q, src, idx_src), (o[1], src, idx_src), (o[2], cache, idx_src),
+                                        (q, cache, idx)], 1):
+            hs2.hs2_sparse_attn_q4(a, c, at, x, y, shape, stream=torch.cuda.default_stream())
+            torch.cuda.synchronize()
+            assert torch.equal(x, o[i]) and torch.equal(y, lse[i]), f"call {i}"
+        hs2.hs2_cache_write_q4(rows[:, :H], rows[:, H:], slot, full, shape)
+        assert torch.equal(full, cache)
+    assert hs2.hs2_get_device_status() == hs2.OK
