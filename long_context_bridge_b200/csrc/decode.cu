@@ -614,13 +614,15 @@ __global__ void __launch_bounds__(256)
   constexpr uint32_t LISTC = 1024;
   __shared__ uint2 s_list[LISTC];
   __shared__ uint32_t s_n, s_base;
+  __shared__ bool s_full;
   grid_wait();
   grid_trigger();
   const int c = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int N = seq_len.n[b];
   const int64_t s_lo = seq_len.lo[b];
   const int64_t s_hi = min(int64_t(N) - w, int64_t(seq_len.hi[b]));  // slice candidates [s_lo, s_hi)
-  if (s_hi - s_lo <= k) return;  // every candidate is selected; decode_final writes them
+  // every candidate is selected (decode_final writes them), or none is
+  if (s_hi - s_lo <= k || k == 0) return;
   const int64_t j_lo = s_lo + int64_t(c) * ch;
   const int64_t j_hi = min(j_lo + ch, s_hi);
   if (j_lo >= j_hi) return;
@@ -628,7 +630,10 @@ __global__ void __launch_bounds__(256)
   const int kb = block_kth_bucket(hist + bg * NBUCKET, uint32_t(k));
   const uint32_t thr = kb < 0 ? 0u : uint32_t(kb);
   const float* sc = score + bg * cap;  // score of key j at sc[j - s_lo]
-  if (threadIdx.x == 0) s_n = 0;
+  if (threadIdx.x == 0) {
+    s_n = 0;
+    s_full = false;
+  }
   __syncthreads();
   const bool vec = (cap & 3) == 0;  // rows of scores start 16-byte aligned
   // in local indices x = j - s_lo: rounds of 2048 keys from a multiple of 4
@@ -660,9 +665,15 @@ __global__ void __launch_bounds__(256)
         const uint2 r = make_uint2(__float_as_uint(v[e]), uint32_t(xl + s_lo));
         if (p < LISTC) {
           s_list[p] = r;
-        } else {  // more than the list holds: straight to global memory
-          const uint32_t q = atomicAdd(&ccount[bg], 1u);
-          if (q < uint32_t(CAPC)) cand[bg * CAPC + q] = r;
+        } else if (!*const_cast<volatile bool*>(&s_full)) {
+          // more than the list holds: straight to global memory, one atomic for
+          // the lanes that are here, and none once decode_final will pass the
+          // candidates over (their count has left the capacity)
+          const uint32_t here = __activemask();
+          uint32_t q = 0;
+          if (lane_id() == __ffs(here) - 1) q = atomicAdd(&ccount[bg], uint32_t(__popc(here)));
+          q = __shfl_sync(here, q, __ffs(here) - 1) + __popc(here & ((1u << lane_id()) - 1u));
+          if (q < uint32_t(CAPC)) cand[bg * CAPC + q] = r; else s_full = true;
         }
       }
     }
