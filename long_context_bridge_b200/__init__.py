@@ -334,10 +334,12 @@ def _on(t, dtype, what, dev):
 
 
 def _shaped(t, shape, what):
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if t.shape != shape:
-        raise ValueError(f"{what} must be {shape}, got {tuple(t.shape)}")
+    try:
+        size = t.shape
+    except AttributeError:
+        raise ValueError(f"{what} must be a CUDA tensor") from None
+    if size != shape:
+        raise ValueError(f"{what} must be {shape}, got {tuple(size)}")
 
 
 def _run(fn, what, dev, stream, args):
@@ -376,7 +378,10 @@ def _rows(t, n, n_heads, what, dev):
 
 
 def _row_args(K, V, slot, n_heads, dev):
-    n = len(K) if isinstance(K, torch.Tensor) and K.dim() else 0
+    try:
+        n = len(K)
+    except TypeError:  # no tensor, or one without rows: _rows says so
+        n = 0
     k, ldk = _rows(K, n, n_heads, "K", dev)
     v, ldv = _rows(V, n, n_heads, "V", dev)
     if slot is not None:
