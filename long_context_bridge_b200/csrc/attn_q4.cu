@@ -13,29 +13,35 @@
 // the partials.
 //
 // What bounds it: with the arithmetic taken out the copies alone run at 6.6
-// TB/s; with it, two contexts of 1M tokens (32 / 4 heads, 1.18 GB) take 224 us =
-// 5.3 TB/s, 0.82 of the measured copy rate, in short bursts (258 us under
-// sustained load, where the power cap lowers the clock).  Per 16 tokens a warp issues about
-// 300 instructions, 145 of them on the integer pipe (one mask per pair of
-// codes), where HBM would leave an SM time for about 390 issue slots per
-// scheduler quarter; the integer pipe is 54% and the issue slots 59% busy, and
-// dependent latencies fill the rest.  Three CTAs of four warps per SM at 168
-// registers: two CTAs 286 us, four (128 registers, spills) 294 us where three
-// took 266; five warps per CTA 23% slower, six or seven 9% to 37%.  Steps of 32
-// keys rather than 16 (266 against 287 us) give the scheduler two independent
-// chains.  Tried and slower: the -8 of V's codes through a second MMA on a
-// constant operand (254 against 244 us), the shifts as multiply-high (247
-// against 228), q^T K as e4m3 MMAs with q split in two (291 against 228; the
-// legacy FP8 MMA is slow here), the queries' fragments in shared memory (equal
-// at 12 warps, 243 against 227 us at 16).
+// TB/s; with it, two contexts of 1M tokens (32 / 4 heads, 1.18 GB) take 227 us =
+// 5.2 TB/s, 0.81 of the measured copy rate, in short bursts (260 us under
+// sustained load, where the power cap lowers the clock).  Per 16 tokens a warp
+// issues 311 instructions, about 140 of them on the integer pipe (one mask per
+// pair of codes), where HBM would leave an SM time for about 390 issue slots per
+// scheduler quarter.  No pipe is saturated (integer 55%, issue slots 60% busy):
+// dependent latencies take part of the rest, and the end of the launch another,
+// since an SM's three CTAs do not end together (see Cut).  Three CTAs of four
+// warps per SM at 168 registers: two CTAs 286 us, four (128 registers, spills)
+// 294 us where three took 266; five warps per CTA 23% slower, six or seven 9%
+// to 37%.  Steps of 32 keys rather than 16 (266 against 287 us) give the
+// scheduler two independent chains.  Tried and slower: the -8 of V's codes
+// through a second MMA on a constant operand (254 against 244 us), the shifts
+// as multiply-high (247 against 228), q^T K as e4m3 MMAs with q split in two
+// (291 against 228; the legacy FP8 MMA is slow here), the queries' fragments in
+// shared memory (equal at 12 warps, 243 against 227 us at 16).
 //
 // sparse_q4: a cluster of CTAs per (sequence, KV head) splits the list; each
 // warp gathers 32 records at a time into a ring of its own by 16-byte
 // asynchronous copies, and the cluster joins through distributed shared memory.
 // One bulk copy per 144-byte record was limited by the rate at which an SM
 // starts bulk copies, about one per 20 cycles (300 x 4 lists of 1152: 100 us,
-// against 68 us).  Few lists are bound by latency (list entry -> record -> step
-// -> join), many by the same instructions as above.
+// against 68 us).  Few short lists are bound by latency (list entry -> record ->
+// step -> join).  From some 48 x 2 lists on the steps get slower as warps are
+// added (1.7 us a step with one CTA per list, 2.7 us with two), which no single
+// counter explains: a warp issues 440 instructions per 16 records (130 more than
+// above, for addresses and copies), issue slots 47% and the integer pipe 39%
+// busy, and L2 is asked for 9.6 sectors of 32 bytes per record (a copy of 16
+// bytes asks for one) where a record covers 5.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -182,8 +188,9 @@ __device__ __forceinline__ void tile_next(TileAt& a, const int* s_pre, const Q4L
 // do not end together (167, 191 and 215 us of 2 x 1M tokens: the first one
 // issues first), but shares of 9 : 8 : 7 in the order of launch made SMs end
 // apart instead (195 to 227 us), since that order does not tell which CTAs
-// share an SM; tiles drawn from a counter would make the order of the sums, and
-// with it the result's last bits, depend on timing.
+// share an SM.  Tiles drawn one by one from a counter into a CTA's partial would
+// make the order of the sums, and with it the result's last bits, depend on
+// timing; drawing fixed chunks with a partial each would not, and is not built.
 struct Cut {
   int total, n;
   __device__ Cut(int tiles, int ctas) : total(tiles), n(min(tiles, ctas)) {}

@@ -607,7 +607,8 @@ __device__ int block_kth_bucket(const uint32_t* __restrict__ gh, uint32_t k) {
 // decode_collect: grid (chunks of ch keys, Hkv, B), 256 threads
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256)
-    decode_collect(const float* __restrict__ score, const uint32_t* __restrict__ hist, SeqLens seq_len, int64_t cap, int Hkv, int k, int w, int ch,
+    decode_collect(const float* __restrict__ score, const uint32_t* __restrict__ hist,
+                   SeqLens seq_len, int64_t cap, int Hkv, int k, int w, int ch,
                    uint2* __restrict__ cand, uint32_t* __restrict__ ccount) {
   // candidates gather here first, so that a CTA takes its place in the (b, g)
   // list with one atomic
@@ -782,7 +783,7 @@ __device__ KeyCut block_top_k(const uint64_t* s, int n, uint32_t k, uint32_t* s_
 }
 
 // Ascending sort of s[0 .. np), np a power of two, in place: a bitonic network
-// whose steps within a warp's 2 np / 16 words need no CTA barrier.  512 threads.
+// whose steps within a warp's max(64, np / 16) words need no CTA barrier.  512 threads.
 __device__ void block_sort_u32(uint32_t* s, int np) {
   const int lane = lane_id(), warp = warp_id();
   const int seg = max(64, np / 16);  // words per warp
@@ -899,8 +900,10 @@ __global__ void __launch_bounds__(512)
     __syncthreads();
     for (int e0 = 0; e0 < int(n); e0 += blockDim.x) {
       const int e = e0 + tid;
-      const bool take = e < int(n) && (n <= uint32_t(k) || (cut.copies > 0 ? sk[e] > cut.prefix
-                                                                           : (sk[e] >> cut.shift) >= (cut.prefix >> cut.shift)));
+      bool take = e < int(n);
+      if (take && n > uint32_t(k))
+        take = cut.copies > 0 ? sk[e] > cut.prefix
+                              : (sk[e] >> cut.shift) >= (cut.prefix >> cut.shift);
       const uint32_t bal = __ballot_sync(0xffffffffu, take);
       uint32_t at = 0;
       if (lane_id() == 0 && bal) at = atomicAdd(&s_misc[3], uint32_t(__popc(bal)));

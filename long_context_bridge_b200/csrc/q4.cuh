@@ -420,8 +420,8 @@ __device__ __forceinline__ void q4_step(Q4State<NT>& st, const uint8_t* rec, uin
       }
     }
     // ---- O^T: per group two 16-dim tiles; nibble j of a half word = tile j / 2,
-    // row gid + 8 (j % 2).  f16 bits 0x6400 | u = 1024 + u, 0x6400 | u << 4 =
-    // 1024 + 16 u.  vw: V words of keys 2t, 2t + 1, 2t + 8, 2t + 9
+    // row gid + 8 (j % 2).  The usual expansion of small integers through f16's
+    // exponent: bits 0x6400 | u = 1024 + u, 0x6400 | u << 4 = 1024 + 16 u.  vw: V words of keys 2t, 2t + 1, 2t + 8, 2t + 9
     uint2 vw[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
