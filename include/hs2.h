@@ -366,7 +366,7 @@ hs2_status hs2_cache_read_q4(const hs2_q4* cache, const int32_t* slot, int64_t f
  * K^, V^ the cache's values as above, for head h of KV head g = h / G:
  *   s_t = scale * q[b,h] . K^[b,g,t]   (0 <= t < seq_len[b])
  *   lse[b,h] = ln sum_t exp(s_t),  o[b,h] = sum_t exp(s_t - lse[b,h]) V^[b,g,t]
- * q, o [batch, n_q_heads, 128] bf16, |q| below 2^110; lse [batch, n_q_heads]
+ * q, o [batch, n_q_heads, 128] bf16, scale * |q| below 2^117; lse [batch, n_q_heads]
  * fp32.  The logits, taken to base 2, are held in fp32 and have to be finite
  * there.  seq_len: DEVICE int32 [batch], read when the call runs (a captured
  * step replays with the lengths of the moment); 0 is a batch row without

@@ -257,7 +257,8 @@ __device__ __forceinline__ void q4_init(Q4State<NT>& st, const __nv_bfloat16* q,
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      st.f[nt][i] = (scale_log2 * 16777216.f) * __shfl_sync(0xffffffffu, back, 4 * (2 * t + i));
+      // finite for scale * |q| below 2^117, in this order for every scale
+      st.f[nt][i] = (scale_log2 * __shfl_sync(0xffffffffu, back, 4 * (2 * t + i))) * 16777216.f;
       st.ref[nt][i] = st.top[nt][i] = -INFINITY;
       st.l[nt][i] = 0.f;
     }

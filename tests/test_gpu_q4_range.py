@@ -134,6 +134,27 @@ def test_random_large_logits(hs2, mul):
     assert apart >= draws * Hq      # of 2 * draws * Hq comparisons
 
 
+@pytest.mark.parametrize("qmul,kmul,scale", [(2.0 ** -60, 2.0 ** -60, 2.0 ** 115), (2.0 ** -100, 2.0 ** -20, 2.0 ** 117),
+                                             (2.0 ** 100, 2.0 ** -110, 2.0 ** 8), (2.0 ** 115, 2.0 ** -112, None),
+                                             (2.0 ** -125, 2.0 ** 115, 2.0 ** 8), (2.0 ** 20, 2.0 ** 90, 2.0 ** -112)])
+def test_scales_of_any_size(hs2, qmul, kmul, scale):
+    """Logits of order 10 from factors at the ends of fp32."""
+    n, Hq = 300, 8
+    rng = np.random.default_rng(9)
+    scale = 128 ** -0.5 if scale is None else scale
+    sc = np.float64(np.float32(scale))
+    rec = ref.records(ref.to_bf16_bits(rng.standard_normal((1, n, 128)) * kmul), ref.to_bf16_bits(rng.standard_normal((1, n, 128))))
+    q = dev_bf16(ref.to_bf16_bits(rng.standard_normal((1, Hq, 128)) * qmul))
+    qh = host_f64(q)
+    idx = rng.permutation(n)[None, None]
+    ob, lb, lists, osb = block(hs2, rec[None], [n], q, scale, 30, 20)
+    for what, (o, lse) in (("attention", attend(hs2, rec[None], [n], q, scale)), ("block", (ob, lb)),
+                           ("list", sparse(hs2, rec[None], idx, q, scale))):
+        ref.check(o[0], lse[0], qh[0], rec[0], sc, what)
+    at = lists[0, 0]
+    ref.check(osb[0], ref.attend(qh[0], rec[0, at], sc)[1], qh[0], rec[0, at], sc, "sparse layer")
+
+
 def check_groups(o, q, rec, scale, what):
     """o [G, 128] against the definition, each group of 32 dims for itself: the
     bound of q4_reference.check with the absolute term of f16's end taken from
