@@ -324,7 +324,8 @@ hs2_status hs2_block_decode(int32_t batch, const int64_t* seq_len, const hs2_bf1
  * (write) or the row of K and V (read) stays as it was.  The slots of one
  * write must be distinct (of a slot listed twice the record is unspecified).
  * n == 0 is valid and launches nothing.  Writing never reads the cache; K and
- * V may not overlap it.  No workspace.  batch * T <= 2^31 - 1.
+ * V may not overlap it.  No workspace.  batch * T <= 2^31 - 1 and n_kv_heads <=
+ * 65535, here and in every call over the 4-bit cache (HS2_ERR_UNSUPPORTED).
  *
  * e4m3 cache (that of hs2_block_decode): Kc, Vc [batch, T, n_kv_heads, 128],
  * scale [batch, T, n_kv_heads] fp32, by the rule of hs2_bridge_kv_fp8; a row
